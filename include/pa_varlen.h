@@ -35,7 +35,13 @@ extern "C" {
 #endif
 
 /* Element types of a tensor descriptor. */
-typedef enum pa_dtype { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2, PA_I32 = 3 } pa_dtype;
+typedef enum pa_dtype {
+    PA_F16 = 0,
+    PA_BF16 = 1,
+    PA_F32 = 2,
+    PA_I32 = 3,
+    PA_E4M3 = 4 /* 8-bit floating point, 4 exponent and 3 mantissa bits, no infinities (8-bit caches) */
+} pa_dtype;
 
 /* A borrowed strided tensor: `data` is a device address (the caller owns it and
  * keeps it alive until the stream has finished the call); `shape` and `stride`
@@ -261,6 +267,88 @@ int pa_kv_append_check(const pa_tensor* k_new, const pa_tensor* v_new, const pa_
                        const pa_tensor* v_cache, int32_t page_block_size);
 
 /*
+ * pa_kv_append_rope -- pa_kv_append with the position rotation applied on the way: one call
+ * rotates the step's q and k by their tokens' positions, writes k and v into their pages and q
+ * to q_out, ready for the attention call that follows.  (The pages have no counterpart; candle
+ * applies the same rotation in an operation of its own before the cache.)
+ *
+ * A token's position is its logical key pos = sk_b - n_b + t, as for pa_kv_append.  With rot =
+ * 2 x cos.shape[1] rotated columns, c = cos[pos] and s = sin[pos], pair i < rot / 2 of every
+ * head of q and k becomes
+ *     (a, b) -> (a c_i - b s_i, b c_i + a s_i)
+ * with (a, b) columns (i, i + rot / 2), or (2 i, 2 i + 1) when `interleaved` is non-zero;
+ * columns at or past rot are copied.  The arithmetic is fp32, rounded once to the tensors' type.
+ *
+ *  q            (total_new, num_heads, head_dim) or NULL; any number of heads; rotated into
+ *  q_out        the same shape (NULL exactly when q is); may be q itself (in place), but not
+ *               overlap it otherwise
+ *  cos, sin     f32 (max_position, rot / 2), last dim contiguous, rows 16-byte aligned;
+ *               0 < rot <= head_dim, a multiple of 16
+ *  k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache,
+ *  page_block_size, stream   as for pa_kv_append
+ * Host checks: those of pa_kv_append, then cos / sin (PA_ERR_RANK, _NONCONTIG, _SHAPE,
+ * _NOT_DEVICE, _ARG for a dtype other than f32, _UNSUPPORTED), then q / q_out likewise.
+ * Rows of q, k_new and v_new at or past cu_seqlens_new[batch] are not read, and their rows of
+ * q_out stay as they are.  On the device, a token whose sequence has more new tokens than keys or
+ * whose position is outside the tables is skipped, one whose page is outside the block table or
+ * the pool has only its q rotated; both are reported as PA_ERR_DEVICE_BOUNDS.  Two tokens of
+ * a call must not name the same slot (a block that the table gives to two sequences): which of
+ * them stays is not defined.
+ */
+int pa_kv_append_rope(const pa_tensor* q, const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* cos,
+                      const pa_tensor* sin, int32_t interleaved, const pa_tensor* cu_seqlens_new,
+                      const pa_tensor* cu_seqlens_k, const pa_tensor* block_table, const pa_tensor* k_cache,
+                      const pa_tensor* v_cache, int32_t page_block_size, const pa_tensor* q_out, void* stream);
+
+/* The host-side checks of pa_kv_append_rope alone: no device-residency check, no CUDA call. */
+int pa_kv_append_rope_check(const pa_tensor* q, const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* cos,
+                            const pa_tensor* sin, int32_t interleaved, const pa_tensor* cu_seqlens_new,
+                            const pa_tensor* cu_seqlens_k, const pa_tensor* block_table, const pa_tensor* k_cache,
+                            const pa_tensor* v_cache, int32_t page_block_size, const pa_tensor* q_out);
+
+/*
+ * pa_kv_append_q8 -- pa_kv_append_rope into caches held in 8 bits: e4m3 codes with one f32
+ * scale for each page and kv head of K and of V, an element's value being code x scale.
+ *
+ * The keys (rotated in fp32, not rounded in between) and values that a call adds to a page give,
+ * for each kv head, the power of two 2^k with the least k >= -100 for which their largest finite
+ * absolute value is at most 448 x 2^k.  A page whose slot 0 is among the new tokens takes that as
+ * its scale; a page that already holds tokens of the sequence keeps the larger of it and its
+ * own scale, and its earlier tokens are held again under the new one when it grew.  Every code
+ * is its value / scale rounded to the nearest e4m3 (ties to even); values that are not finite
+ * become NaN.  Slots past the sequence's last key, and other pages, stay as they are.
+ *
+ *  cos, sin     as for pa_kv_append_rope, or both NULL: no rotation, and then q must be NULL
+ *  k_cache,
+ *  v_cache      e4m3 (num_blocks, page_block_size, num_heads_k, head_dim), same shape and
+ *               strides, last dim contiguous, the others multiples of 16; head_dim a
+ *               multiple of 16
+ *  k_scale,
+ *  v_scale      f32 (num_blocks, num_heads_k), any positive strides; written for the pages
+ *               that receive tokens, read for those that already hold some
+ *  the rest     as for pa_kv_append_rope
+ * Host checks: those of pa_kv_append (the caches' dtype aside), then the caches' dtype, the
+ * scales (PA_ERR_RANK, _SHAPE, _NOT_DEVICE, _ARG, _UNSUPPORTED), head_dim and strides
+ * (_UNSUPPORTED), then those of pa_kv_append_rope.  On the device, bad metadata is reported as
+ * PA_ERR_DEVICE_BOUNDS: a sequence with more new tokens than keys is skipped, a page outside the
+ * block table, the pool or (its last new token) the tables is left as it is, and a q row
+ * whose position is outside the tables is not written.  A block must not be given to two
+ * sequences that both add tokens to it: its contents are then not defined.
+ */
+int pa_kv_append_q8(const pa_tensor* q, const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* cos,
+                    const pa_tensor* sin, int32_t interleaved, const pa_tensor* cu_seqlens_new,
+                    const pa_tensor* cu_seqlens_k, const pa_tensor* block_table, const pa_tensor* k_cache,
+                    const pa_tensor* v_cache, const pa_tensor* k_scale, const pa_tensor* v_scale,
+                    int32_t page_block_size, const pa_tensor* q_out, void* stream);
+
+/* The host-side checks of pa_kv_append_q8 alone: no device-residency check, no CUDA call. */
+int pa_kv_append_q8_check(const pa_tensor* q, const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* cos,
+                          const pa_tensor* sin, int32_t interleaved, const pa_tensor* cu_seqlens_new,
+                          const pa_tensor* cu_seqlens_k, const pa_tensor* block_table, const pa_tensor* k_cache,
+                          const pa_tensor* v_cache, const pa_tensor* k_scale, const pa_tensor* v_scale,
+                          int32_t page_block_size, const pa_tensor* q_out);
+
+/*
  * pa_fwd_padded -- attention over a padded batch (every sequence of the batch has seqlen_q
  * queries and seqlen_k keys), the non-varlen API the pages point to for padded batches
  * ("flash-attn-varlen expects input tensors of rank 3", Solutions: use FlashAttention
@@ -329,8 +417,8 @@ uint64_t pa_kernel_launches(void);
  * milliseconds and to launches[c] the number of timed launches of kernel class c, and
  * clears the record.  Classes: PA_KC_PREFILL (the tensor-core prefill kernels),
  * PA_KC_SPLITKV (the split-KV pass: decode_kernel, decode512_kernel, decode_tc_kernel or
- * splitkv_kernel), PA_KC_COMBINE (the split-KV combine), PA_KC_APPEND (pa_kv_append's
- * kernel).  ms and launches are caller-owned host arrays of PA_KERNEL_CLASSES entries.  Returns PA_OK, PA_ERR_ARG for a null array, or PA_ERR_CUDA if an event
+ * splitkv_kernel), PA_KC_COMBINE (the split-KV combine), PA_KC_APPEND (the appends'
+ * kernels).  ms and launches are caller-owned host arrays of PA_KERNEL_CLASSES entries.  Returns PA_OK, PA_ERR_ARG for a null array, or PA_ERR_CUDA if an event
  * query failed (message in pa_last_error; the record is cleared either way). */
 #define PA_KC_PREFILL 0
 #define PA_KC_SPLITKV 1

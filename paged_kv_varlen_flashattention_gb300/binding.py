@@ -16,7 +16,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "libpa_varlen.so")
 _lib = None
 
-PA_F16, PA_BF16, PA_F32, PA_I32 = 0, 1, 2, 3
+PA_F16, PA_BF16, PA_F32, PA_I32, PA_E4M3 = 0, 1, 2, 3, 4
 
 STATUS = {
     0: "PA_OK", 1: "PA_ERR_RANK", 2: "PA_ERR_RANK_PAGED", 3: "PA_ERR_NONCONTIG", 4: "PA_ERR_SHAPE",
@@ -84,6 +84,16 @@ def load():
         lib.pa_kv_append.argtypes = [_TP] * 7 + [ctypes.c_int32, ctypes.c_void_p]
         lib.pa_kv_append_check.restype = ctypes.c_int
         lib.pa_kv_append_check.argtypes = [_TP] * 7 + [ctypes.c_int32]
+        _ROPE = [_TP] * 5 + [ctypes.c_int32] + [_TP] * 5 + [ctypes.c_int32, _TP]
+        lib.pa_kv_append_rope.restype = ctypes.c_int
+        lib.pa_kv_append_rope.argtypes = _ROPE + [ctypes.c_void_p]
+        lib.pa_kv_append_rope_check.restype = ctypes.c_int
+        lib.pa_kv_append_rope_check.argtypes = list(_ROPE)
+        _Q8 = [_TP] * 5 + [ctypes.c_int32] + [_TP] * 7 + [ctypes.c_int32, _TP]
+        lib.pa_kv_append_q8.restype = ctypes.c_int
+        lib.pa_kv_append_q8.argtypes = _Q8 + [ctypes.c_void_p]
+        lib.pa_kv_append_q8_check.restype = ctypes.c_int
+        lib.pa_kv_append_q8_check.argtypes = list(_Q8)
         _PAD = [_TP, _TP, _TP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, ctypes.c_int32,
                 ctypes.c_int32, _TP, _TP, _TP]
         lib.pa_fwd_padded.restype = ctypes.c_int
@@ -105,7 +115,8 @@ def _dtype_code(t) -> int:
     global _DTYPE_CODES
     if _DTYPE_CODES is None:
         import torch
-        _DTYPE_CODES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32, torch.int32: PA_I32}
+        _DTYPE_CODES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32, torch.int32: PA_I32,
+                        torch.float8_e4m3fn: PA_E4M3}
     return _DTYPE_CODES.get(t.dtype, -1)
 
 
@@ -252,6 +263,62 @@ def kv_append(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, 
 def kv_append_check(descriptors, page_block_size) -> int:
     """Host-only checks of pa_kv_append on seven descriptors (PaTensor or None)."""
     return load().pa_kv_append_check(*[_ref(d) for d in descriptors], int(page_block_size))
+
+
+def kv_append_rope(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, cos, sin, q=None,
+                   q_out=None, interleaved=False, page_block_size=None, stream=None):
+    """pa_kv_append_rope on torch CUDA tensors: rotates ``k_new`` (and ``q`` when given) by
+    the tokens' positions with the tables ``cos`` / ``sin`` (max_position, rot / 2) fp32,
+    and writes k and v into their pages, in place.  Returns the rotated q (``q_out``,
+    allocated with torch when not given; pass ``q`` itself to rotate in place) or None."""
+    import torch
+    lib = load()
+    P = page_block_size if page_block_size is not None else k_cache.shape[1]
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    s = stream if stream is not None else torch.cuda.current_stream(k_new.device)
+    ds = [_ref(describe(t)) for t in (q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache,
+                                      v_cache, q_out)]
+    rc = lib.pa_kv_append_rope(*ds[:5], 1 if interleaved else 0, *ds[5:10], int(P), ds[10],
+                               ctypes.c_void_p(s.cuda_stream))
+    if rc != 0:
+        raise PaError(rc, lib.pa_last_error().decode())
+    return q_out
+
+
+def kv_append_rope_check(descriptors, page_block_size, interleaved=False) -> int:
+    """Host-only checks of pa_kv_append_rope on the descriptors (PaTensor or None) of q, k_new,
+    v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, q_out."""
+    d = [_ref(x) for x in descriptors]
+    return load().pa_kv_append_rope_check(*d[:5], 1 if interleaved else 0, *d[5:10], int(page_block_size), d[10])
+
+
+def kv_append_q8(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, k_scale, v_scale,
+                 cos=None, sin=None, q=None, q_out=None, interleaved=False, page_block_size=None, stream=None):
+    """pa_kv_append_q8 on torch CUDA tensors: as :func:`kv_append_rope`, into caches of
+    ``torch.float8_e4m3fn`` codes with the fp32 scales ``k_scale`` / ``v_scale``
+    (num_blocks, num_heads_k) of every page and kv head, updated in place.  Without ``cos`` and
+    ``sin`` the keys are held as they are (and ``q`` must not be given)."""
+    import torch
+    lib = load()
+    P = page_block_size if page_block_size is not None else k_cache.shape[1]
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    s = stream if stream is not None else torch.cuda.current_stream(k_new.device)
+    ds = [_ref(describe(t)) for t in (q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache,
+                                      v_cache, k_scale, v_scale, q_out)]
+    rc = lib.pa_kv_append_q8(*ds[:5], 1 if interleaved else 0, *ds[5:12], int(P), ds[12],
+                             ctypes.c_void_p(s.cuda_stream))
+    if rc != 0:
+        raise PaError(rc, lib.pa_last_error().decode())
+    return q_out
+
+
+def kv_append_q8_check(descriptors, page_block_size, interleaved=False) -> int:
+    """Host-only checks of pa_kv_append_q8 on the descriptors (PaTensor or None) of q, k_new, v_new,
+    cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, k_scale, v_scale, q_out."""
+    d = [_ref(x) for x in descriptors]
+    return load().pa_kv_append_q8_check(*d[:5], 1 if interleaved else 0, *d[5:12], int(page_block_size), d[12])
 
 
 def fwd_padded(q, k, v, softmax_scale=None, window_left=-1, window_right=0, alibi_slopes=None, out=None,

@@ -386,6 +386,146 @@ int validate_append(const pa_tensor* kn, const pa_tensor* vn, const pa_tensor* c
     return PA_OK;
 }
 
+// ---- KV append with the position rotation (16-bit or 8-bit cache): host checks ---------------
+// cos and sin may both be NULL for the 8-bit cache (no rotation, and then no q).
+int validate_rope(const pa_tensor* q, const pa_tensor* kn, const pa_tensor* vn, const pa_tensor* cos,
+                  const pa_tensor* sin, const pa_tensor* q_out, bool tables_optional, bool check_device,
+                  pa::RopeArgs* a) {
+    const int64_t D = kn->shape[2], total = kn->shape[0];
+    auto on_device = [&](const pa_tensor* t) { return !check_device || numel(t) == 0 || is_device_memory(t->data); };
+    a->dtype = kn->dtype;
+    if ((cos == nullptr) != (sin == nullptr)) return fail(PA_ERR_ARG, "cos and sin must be given together");
+    if (!cos && !tables_optional) return fail(PA_ERR_ARG, "a tensor descriptor is NULL (cos and sin are required)");
+    if ((q == nullptr) != (q_out == nullptr)) return fail(PA_ERR_ARG, "q and q_out must be given together");
+    if (q && !cos) return fail(PA_ERR_ARG, "q is only rotated: it needs cos and sin");
+    if (cos) {
+        if (cos->ndim != 2 || sin->ndim != 2)
+            return fail(PA_ERR_RANK, "cos and sin must be of rank 2 (cos: %d, sin: %d)", cos->ndim, sin->ndim);
+        if (cos->stride[1] != 1) return fail(PA_ERR_NONCONTIG, "the last dim of cos must be contiguous %s", strides(cos).c_str());
+        if (sin->stride[1] != 1) return fail(PA_ERR_NONCONTIG, "the last dim of sin must be contiguous %s", strides(sin).c_str());
+        if (!same_shape(cos, sin))
+            return fail(PA_ERR_SHAPE, "shape mismatch cos %s and sin %s", dims(cos).c_str(), dims(sin).c_str());
+        const int64_t rot = 2 * cos->shape[1];
+        if (rot <= 0 || rot > D)
+            return fail(PA_ERR_SHAPE, "cos %s rotates %lld columns of a head_dim of %lld", dims(cos).c_str(),
+                        (long long)rot, (long long)D);
+        if (!on_device(cos)) return fail(PA_ERR_NOT_DEVICE, "cos must be a cuda tensor");
+        if (!on_device(sin)) return fail(PA_ERR_NOT_DEVICE, "sin must be a cuda tensor");
+        if (cos->dtype != PA_F32 || sin->dtype != PA_F32) return fail(PA_ERR_ARG, "cos and sin must be f32");
+        if (rot % 16 != 0)
+            return fail(PA_ERR_UNSUPPORTED, "%lld rotated columns: the kernels need a multiple of 16", (long long)rot);
+        for (const pa_tensor* t : {cos, sin}) {
+            if (numel(t) == 0) continue;
+            if (!aligned16(t->data) || (t->shape[0] > 1 && (t->stride[0] % 4 != 0 || t->stride[0] <= 0)))
+                return fail(PA_ERR_UNSUPPORTED, "cos and sin rows must be 16-byte aligned");
+        }
+        a->cos = static_cast<const float*>(cos->data);
+        a->sin = static_cast<const float*>(sin->data);
+        a->cos_s0 = cos->stride[0];
+        a->sin_s0 = sin->stride[0];
+        a->max_pos = cos->shape[0];
+        a->rot = (int)rot;
+    }
+    if (q) {
+        if (q->ndim != 3 || q_out->ndim != 3)
+            return fail(PA_ERR_RANK, "q and q_out must be of rank 3 (q: %d, q_out: %d)", q->ndim, q_out->ndim);
+        if (q->stride[2] != 1) return fail(PA_ERR_NONCONTIG, "the last dim of q must be contiguous %s", strides(q).c_str());
+        if (q_out->stride[2] != 1)
+            return fail(PA_ERR_NONCONTIG, "the last dim of q_out must be contiguous %s", strides(q_out).c_str());
+        if (q->shape[0] != total || q->shape[2] != D)
+            return fail(PA_ERR_SHAPE, "shape mismatch q %s and k_new %s", dims(q).c_str(), dims(kn).c_str());
+        if (!same_shape(q, q_out))
+            return fail(PA_ERR_SHAPE, "shape mismatch q %s and q_out %s", dims(q).c_str(), dims(q_out).c_str());
+        if (!on_device(q)) return fail(PA_ERR_NOT_DEVICE, "q must be a cuda tensor");
+        if (!on_device(q_out)) return fail(PA_ERR_NOT_DEVICE, "q_out must be a cuda tensor");
+        if (q->dtype != kn->dtype || q_out->dtype != kn->dtype)
+            return fail(PA_ERR_ARG, "q, q_out and k_new must share one dtype");
+        if (q->shape[1] > (1 << 20)) return fail(PA_ERR_UNSUPPORTED, "num_heads %lld", (long long)q->shape[1]);
+        for (const pa_tensor* t : {q, q_out}) {
+            if (numel(t) == 0) continue;
+            if (!aligned16(t->data)) return fail(PA_ERR_UNSUPPORTED, "q and q_out base addresses must be 16-byte aligned");
+            for (int d = 0; d < 2; ++d)
+                if (t->stride[d] % 8 != 0 || t->stride[d] <= 0)
+                    return fail(PA_ERR_UNSUPPORTED, "strides %s: all but the last must be positive multiples of 8 elements",
+                                strides(t).c_str());
+        }
+        a->q = q->data;
+        a->q_out = q_out->data;
+        a->q_s0 = q->stride[0];
+        a->q_s1 = q->stride[1];
+        a->qo_s0 = q_out->stride[0];
+        a->qo_s1 = q_out->stride[1];
+        a->H = (int)q->shape[1];
+    }
+    return PA_OK;
+}
+
+// ---- 8-bit caches: what the 16-bit checks do not cover ----------------------------------------
+// The caches' element type, strides and alignment, and the scales (num_blocks, num_heads_k).
+int check_q8_cache(const pa_tensor* kc, const pa_tensor* vc, const pa_tensor* ks, const pa_tensor* vs,
+                   bool check_device) {
+    if (kc->dtype != PA_E4M3 || vc->dtype != PA_E4M3)
+        return fail(PA_ERR_ARG, "the 8-bit caches must be e4m3 (k %d, v %d)", kc->dtype, vc->dtype);
+    for (const pa_tensor* t : {ks, vs}) {
+        const char* name = t == ks ? "k_scale" : "v_scale";
+        if (t->ndim != 2) return fail(PA_ERR_RANK, "%s must be of rank 2, got rank %d", name, t->ndim);
+        if (t->shape[0] != kc->shape[0] || t->shape[1] != kc->shape[2])
+            return fail(PA_ERR_SHAPE, "shape mismatch %s %s, expected [%lld, %lld]", name, dims(t).c_str(),
+                        (long long)kc->shape[0], (long long)kc->shape[2]);
+        if (check_device && numel(t) != 0 && !is_device_memory(t->data))
+            return fail(PA_ERR_NOT_DEVICE, "%s must be a cuda tensor", name);
+        if (t->dtype != PA_F32) return fail(PA_ERR_ARG, "%s must be f32", name);
+        for (int d = 0; d < 2; ++d)
+            if (t->shape[d] > 1 && t->stride[d] <= 0)
+                return fail(PA_ERR_UNSUPPORTED, "%s strides %s must be positive", name, strides(t).c_str());
+    }
+    if (kc->shape[3] % 16 != 0)
+        return fail(PA_ERR_UNSUPPORTED, "head_dim %lld: an 8-bit cache needs a multiple of 16", (long long)kc->shape[3]);
+    for (const pa_tensor* t : {kc, vc})
+        for (int d = 0; d < 3; ++d)
+            if (numel(t) != 0 && t->stride[d] % 16 != 0)
+                return fail(PA_ERR_UNSUPPORTED, "strides %s: all but the last must be multiples of 16 elements of an 8-bit cache",
+                            strides(t).c_str());
+    return PA_OK;
+}
+
+// The 16-bit checks of a paged k or v descriptor, with the element type in place of its own.
+pa_tensor with_dtype(const pa_tensor* t, int32_t dtype) {
+    pa_tensor c = *t;
+    c.dtype = dtype;
+    return c;
+}
+
+int rope_args(const pa_tensor* q, const pa_tensor* kn, const pa_tensor* vn, const pa_tensor* cos, const pa_tensor* sin,
+              int32_t interleaved, const pa_tensor* cu_new, const pa_tensor* cu_k, const pa_tensor* bt,
+              const pa_tensor* kc, const pa_tensor* vc, int32_t page_block_size, const pa_tensor* q_out,
+              bool check_device, pa::RopeArgs* a) {
+    int rc = validate_append(kn, vn, cu_new, cu_k, bt, kc, vc, page_block_size, check_device, &a->kv);
+    if (rc != PA_OK) return rc;
+    a->interleaved = interleaved != 0;
+    return validate_rope(q, kn, vn, cos, sin, q_out, false, check_device, a);
+}
+
+int q8_append_args(const pa_tensor* q, const pa_tensor* kn, const pa_tensor* vn, const pa_tensor* cos,
+                   const pa_tensor* sin, int32_t interleaved, const pa_tensor* cu_new, const pa_tensor* cu_k,
+                   const pa_tensor* bt, const pa_tensor* kc, const pa_tensor* vc, const pa_tensor* ks,
+                   const pa_tensor* vs, int32_t page_block_size, const pa_tensor* q_out, bool check_device,
+                   pa::RopeArgs* a) {
+    if (!kn || !kc || !vc || !ks || !vs) return fail(PA_ERR_ARG, "a tensor descriptor is NULL");
+    const pa_tensor k16 = with_dtype(kc, kn->dtype), v16 = with_dtype(vc, kn->dtype);
+    int rc = validate_append(kn, vn, cu_new, cu_k, bt, &k16, &v16, page_block_size, check_device, &a->kv);
+    if (rc != PA_OK) return rc;
+    if ((rc = check_q8_cache(kc, vc, ks, vs, check_device)) != PA_OK) return rc;
+    a->interleaved = interleaved != 0;
+    a->k_scale = static_cast<float*>(ks->data);
+    a->v_scale = static_cast<float*>(vs->data);
+    a->ks_s0 = ks->stride[0];
+    a->ks_s1 = ks->stride[1];
+    a->vs_s0 = vs->stride[0];
+    a->vs_s1 = vs->stride[1];
+    return validate_rope(q, kn, vn, cos, sin, q_out, true, check_device, a);
+}
+
 // ---- per-(device, stream) split-KV workspace ------------------------------------------------
 std::mutex g_ws_mu;
 std::map<std::pair<int, cudaStream_t>, pa::Workspace> g_ws;
@@ -949,6 +1089,63 @@ int pa_kv_append(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor
     int ce = pa::error_word(&err);
     if (ce != cudaSuccess) return fail(PA_ERR_CUDA, "error word: %s", cudaGetErrorString((cudaError_t)ce));
     rc = pa::launch_kv_append(a, err, g_msg, sizeof g_msg);
+    if (rc == PA_OK) g_msg[0] = '\0';
+    return rc;
+}
+
+// ---- append with the position rotation, and into an 8-bit cache ----
+int pa_kv_append_rope_check(const pa_tensor* q, const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* cos,
+                            const pa_tensor* sin, int32_t interleaved, const pa_tensor* cu_seqlens_new,
+                            const pa_tensor* cu_seqlens_k, const pa_tensor* block_table, const pa_tensor* k_cache,
+                            const pa_tensor* v_cache, int32_t page_block_size, const pa_tensor* q_out) {
+    pa::RopeArgs a{};
+    return rope_args(q, k_new, v_new, cos, sin, interleaved, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache,
+                     page_block_size, q_out, false, &a);
+}
+
+int pa_kv_append_rope(const pa_tensor* q, const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* cos,
+                      const pa_tensor* sin, int32_t interleaved, const pa_tensor* cu_seqlens_new,
+                      const pa_tensor* cu_seqlens_k, const pa_tensor* block_table, const pa_tensor* k_cache,
+                      const pa_tensor* v_cache, int32_t page_block_size, const pa_tensor* q_out, void* stream) {
+    pa::NvtxRange range("pa_kv_append_rope");
+    pa::RopeArgs a{};
+    int rc = rope_args(q, k_new, v_new, cos, sin, interleaved, cu_seqlens_new, cu_seqlens_k, block_table, k_cache,
+                       v_cache, page_block_size, q_out, true, &a);
+    if (rc != PA_OK) return rc;
+    a.kv.stream = static_cast<cudaStream_t>(stream);
+    unsigned int* err = nullptr;
+    int ce = pa::error_word(&err);
+    if (ce != cudaSuccess) return fail(PA_ERR_CUDA, "error word: %s", cudaGetErrorString((cudaError_t)ce));
+    rc = pa::launch_rope_append(a, err, g_msg, sizeof g_msg);
+    if (rc == PA_OK) g_msg[0] = '\0';
+    return rc;
+}
+
+int pa_kv_append_q8_check(const pa_tensor* q, const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* cos,
+                          const pa_tensor* sin, int32_t interleaved, const pa_tensor* cu_seqlens_new,
+                          const pa_tensor* cu_seqlens_k, const pa_tensor* block_table, const pa_tensor* k_cache,
+                          const pa_tensor* v_cache, const pa_tensor* k_scale, const pa_tensor* v_scale,
+                          int32_t page_block_size, const pa_tensor* q_out) {
+    pa::RopeArgs a{};
+    return q8_append_args(q, k_new, v_new, cos, sin, interleaved, cu_seqlens_new, cu_seqlens_k, block_table, k_cache,
+                          v_cache, k_scale, v_scale, page_block_size, q_out, false, &a);
+}
+
+int pa_kv_append_q8(const pa_tensor* q, const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor* cos,
+                    const pa_tensor* sin, int32_t interleaved, const pa_tensor* cu_seqlens_new,
+                    const pa_tensor* cu_seqlens_k, const pa_tensor* block_table, const pa_tensor* k_cache,
+                    const pa_tensor* v_cache, const pa_tensor* k_scale, const pa_tensor* v_scale,
+                    int32_t page_block_size, const pa_tensor* q_out, void* stream) {
+    pa::NvtxRange range("pa_kv_append_q8");
+    pa::RopeArgs a{};
+    int rc = q8_append_args(q, k_new, v_new, cos, sin, interleaved, cu_seqlens_new, cu_seqlens_k, block_table, k_cache,
+                            v_cache, k_scale, v_scale, page_block_size, q_out, true, &a);
+    if (rc != PA_OK) return rc;
+    a.kv.stream = static_cast<cudaStream_t>(stream);
+    unsigned int* err = nullptr;
+    int ce = pa::error_word(&err);
+    if (ce != cudaSuccess) return fail(PA_ERR_CUDA, "error word: %s", cudaGetErrorString((cudaError_t)ce));
+    rc = pa::launch_q8_append(a, err, g_msg, sizeof g_msg);
     if (rc == PA_OK) g_msg[0] = '\0';
     return rc;
 }

@@ -46,6 +46,10 @@ struct Args {
     uint64_t wait_ns;    // bound on every in-kernel wait
     int withhold_loads;  // test hook: producers issue no loads
     const float* alibi;  // per-query-head slopes of the linear position bias, or nullptr
+    // 8-bit cache only: the scales of K and V, (num_blocks, Hkv) f32
+    const float* k_scale;
+    const float* v_scale;
+    int64_t ks_s0, ks_s1, vs_s0, vs_s1;
 };
 
 // Scratch the split-KV path needs for a call (bytes), and where to put it.
@@ -143,6 +147,27 @@ struct AppendArgs {
     cudaStream_t stream;
 };
 int launch_kv_append(const AppendArgs& a, unsigned int* err, char* msg, size_t msg_len);
+
+// The append with the position rotation on the way (pa_kv_append_rope, pa_kv_append_q8):
+// the step's q beside its k and v, the rotation tables, and for an 8-bit cache the scales.
+struct RopeArgs {
+    AppendArgs kv;  // k_new, v_new and the caches (element strides; one-byte elements for q8)
+    int dtype;      // PA_F16 or PA_BF16: k_new, v_new, q, q_out
+    const void* q;  // nullptr: no q
+    void* q_out;
+    int64_t q_s0, q_s1, qo_s0, qo_s1;
+    int H;
+    const float* cos;  // (max_pos, rot / 2); nullptr: no rotation (rot = 0)
+    const float* sin;
+    int64_t cos_s0, sin_s0;
+    int64_t max_pos;
+    int rot, interleaved;
+    float* k_scale;  // q8 only: (num_blocks, Hkv)
+    float* v_scale;
+    int64_t ks_s0, ks_s1, vs_s0, vs_s1;
+};
+int launch_rope_append(const RopeArgs& a, unsigned int* err, char* msg, size_t msg_len);
+int launch_q8_append(const RopeArgs& a, unsigned int* err, char* msg, size_t msg_len);
 
 // Per-kernel timing (pa_kernel_timing): timer_begin before a launch of kernel class `cls`
 // (PA_KC_*) into `stream`, timer_end after it launched successfully.  Both do nothing
