@@ -349,6 +349,45 @@ int pa_kv_append_q8_check(const pa_tensor* q, const pa_tensor* k_new, const pa_t
                           int32_t page_block_size, const pa_tensor* q_out);
 
 /*
+ * pa_varlen_fwd_q8 -- pa_varlen_fwd (pa_varlen_fwd_alibi with slopes) over caches held in 8 bits:
+ * K_j = k_scale[blk, hk] x code and V_j = v_scale[blk, hk] x code, blk the physical block of key
+ * j, as pa_kv_append_q8 writes them.  Same mask, GQA mapping, bias, lse and empty rows.
+ *
+ *  q, out        f16 or bf16, as for pa_varlen_fwd
+ *  k_cache,
+ *  v_cache       e4m3 (num_blocks, page_block_size, num_heads_k, head_dim), same shape and
+ *                strides, last dim contiguous, the others multiples of 16; head_dim a multiple
+ *                of 16.  Always paged: block_table must not be NULL
+ *  k_scale,
+ *  v_scale       f32 (num_blocks, num_heads_k), any positive strides; finite and not negative;
+ *                V scales below 2^-100 (and zero) are read as 2^-100
+ *  alibi_slopes  (num_heads,) f32 or NULL
+ *  the rest      as for pa_varlen_fwd
+ * Scores are accumulated in fp32 from exact codes; the softmax weights are rounded to f16 (11
+ * bits) for the product with V, whatever q's type.  A code that is NaN, or a scale that is
+ * NaN, reaches the rows that attend its key; one that no row of a call's tile attends (past the
+ * sequence, before every window) does not matter.
+ * Host checks: those of pa_varlen_fwd (the caches' dtype aside), then the caches' dtype, the
+ * scales, head_dim and strides as for pa_kv_append_q8; PA_ERR_UNSUPPORTED when max_seqlen_k needs
+ * more than 1024 splits of 8192 keys.  Scratch, streams, graph capture and threads as for
+ * pa_varlen_fwd.
+ */
+int pa_varlen_fwd_q8(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* k_scale,
+                     const pa_tensor* v_scale, const pa_tensor* cu_seqlens_q, const pa_tensor* cu_seqlens_k,
+                     const pa_tensor* block_table, int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads,
+                     int32_t num_heads_k, int32_t head_dim, int32_t page_block_size, float softmax_scale,
+                     int32_t window_left, int32_t window_right, const pa_tensor* alibi_slopes, const pa_tensor* out,
+                     const pa_tensor* softmax_lse, void* stream);
+
+/* The host-side checks of pa_varlen_fwd_q8 alone: no device-residency check, no CUDA call. */
+int pa_varlen_check_q8(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* k_scale,
+                       const pa_tensor* v_scale, const pa_tensor* cu_seqlens_q, const pa_tensor* cu_seqlens_k,
+                       const pa_tensor* block_table, int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads,
+                       int32_t num_heads_k, int32_t head_dim, int32_t page_block_size, float softmax_scale,
+                       int32_t window_left, int32_t window_right, const pa_tensor* alibi_slopes, const pa_tensor* out,
+                       const pa_tensor* softmax_lse);
+
+/*
  * pa_fwd_padded -- attention over a padded batch (every sequence of the batch has seqlen_q
  * queries and seqlen_k keys), the non-varlen API the pages point to for padded batches
  * ("flash-attn-varlen expects input tensors of rank 3", Solutions: use FlashAttention

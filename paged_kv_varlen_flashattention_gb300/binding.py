@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -84,16 +85,23 @@ def load():
         lib.pa_kv_append.argtypes = [_TP] * 7 + [ctypes.c_int32, ctypes.c_void_p]
         lib.pa_kv_append_check.restype = ctypes.c_int
         lib.pa_kv_append_check.argtypes = [_TP] * 7 + [ctypes.c_int32]
-        _ROPE = [_TP] * 5 + [ctypes.c_int32] + [_TP] * 5 + [ctypes.c_int32, _TP]
+        # descriptors as addresses: these calls take them packed (see _pack) or by reference
+        _VP = ctypes.c_void_p
+        _ROPE = [_VP] * 5 + [ctypes.c_int32] + [_VP] * 5 + [ctypes.c_int32, _VP]
         lib.pa_kv_append_rope.restype = ctypes.c_int
         lib.pa_kv_append_rope.argtypes = _ROPE + [ctypes.c_void_p]
         lib.pa_kv_append_rope_check.restype = ctypes.c_int
         lib.pa_kv_append_rope_check.argtypes = list(_ROPE)
-        _Q8 = [_TP] * 5 + [ctypes.c_int32] + [_TP] * 7 + [ctypes.c_int32, _TP]
+        _Q8 = [_VP] * 5 + [ctypes.c_int32] + [_VP] * 7 + [ctypes.c_int32, _VP]
         lib.pa_kv_append_q8.restype = ctypes.c_int
         lib.pa_kv_append_q8.argtypes = _Q8 + [ctypes.c_void_p]
         lib.pa_kv_append_q8_check.restype = ctypes.c_int
         lib.pa_kv_append_q8_check.argtypes = list(_Q8)
+        _FWD_Q8 = [_VP] * 8 + _FWD_ARGS[6:15] + [_VP] * 3
+        lib.pa_varlen_fwd_q8.restype = ctypes.c_int
+        lib.pa_varlen_fwd_q8.argtypes = _FWD_Q8 + [ctypes.c_void_p]
+        lib.pa_varlen_check_q8.restype = ctypes.c_int
+        lib.pa_varlen_check_q8.argtypes = list(_FWD_Q8)
         _PAD = [_TP, _TP, _TP, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_float, ctypes.c_int32,
                 ctypes.c_int32, _TP, _TP, _TP]
         lib.pa_fwd_padded.restype = ctypes.c_int
@@ -111,13 +119,17 @@ def load():
 _DTYPE_CODES = None
 
 
-def _dtype_code(t) -> int:
+def _dtype_codes() -> dict:
     global _DTYPE_CODES
     if _DTYPE_CODES is None:
         import torch
         _DTYPE_CODES = {torch.float16: PA_F16, torch.bfloat16: PA_BF16, torch.float32: PA_F32, torch.int32: PA_I32,
                         torch.float8_e4m3fn: PA_E4M3}
-    return _DTYPE_CODES.get(t.dtype, -1)
+    return _DTYPE_CODES
+
+
+def _dtype_code(t) -> int:
+    return _dtype_codes().get(t.dtype, -1)
 
 
 _I64x4 = ctypes.c_int64 * 4
@@ -132,6 +144,47 @@ def describe(t) -> Optional[PaTensor]:
     if n >= 4:
         return PaTensor(t.data_ptr(), _dtype_code(t), n, _I64x4(*shape[:4]), _I64x4(*stride[:4]))
     return PaTensor(t.data_ptr(), _dtype_code(t), n, _I64x4(*shape), _I64x4(*stride))
+
+
+# pa_tensor by rank: data, dtype, ndim, shape[4], stride[4] with zeros behind the rank
+_PACK = [None] + [struct.Struct(f"Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x").pack_into for n in (1, 2, 3, 4)]
+
+
+def _pack(tensors):
+    """(buffer, addresses) of the tensors' descriptors in one buffer that the caller keeps
+    alive over the call; None stays None.  About a third of the host time of one ctypes
+    structure per tensor."""
+    codes = _dtype_codes()
+    buf = bytearray(80 * len(tensors))
+    at = ctypes.addressof(ctypes.c_char.from_buffer(buf))
+    where, off = [], 0
+    for t in tensors:
+        if t is None:
+            where.append(None)
+        else:
+            shape = t.shape
+            n = len(shape)
+            if 1 <= n <= 4:
+                _PACK[n](buf, off, t.data_ptr(), codes.get(t.dtype, -1), n, *shape, *t.stride())
+            else:  # no rank the library takes: the rank alone, for its refusal
+                _PACK[1](buf, off, t.data_ptr(), codes.get(t.dtype, -1), n, 0, 1)
+            where.append(at + off)
+        off += 80
+    return buf, where
+
+
+def _call(fn, on, stream, *args) -> None:
+    """fn(*args, stream) with the device of tensor ``on`` current (its current stream when
+    ``stream`` is None); raises PaError on a non-zero status."""
+    import torch
+    index = on.get_device()
+    if index >= 0 and index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _call(fn, on, stream, *args)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    rc = fn(*args, s.cuda_stream)
+    if rc != 0:
+        raise PaError(rc, load().pa_last_error().decode())
 
 
 def _ref(d):
@@ -276,13 +329,8 @@ def kv_append_rope(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_ca
     P = page_block_size if page_block_size is not None else k_cache.shape[1]
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    s = stream if stream is not None else torch.cuda.current_stream(k_new.device)
-    ds = [_ref(describe(t)) for t in (q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache,
-                                      v_cache, q_out)]
-    rc = lib.pa_kv_append_rope(*ds[:5], 1 if interleaved else 0, *ds[5:10], int(P), ds[10],
-                               ctypes.c_void_p(s.cuda_stream))
-    if rc != 0:
-        raise PaError(rc, lib.pa_last_error().decode())
+    keep, ds = _pack((q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, q_out))
+    _call(lib.pa_kv_append_rope, k_new, stream, *ds[:5], 1 if interleaved else 0, *ds[5:10], int(P), ds[10])
     return q_out
 
 
@@ -304,13 +352,9 @@ def kv_append_q8(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_cach
     P = page_block_size if page_block_size is not None else k_cache.shape[1]
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    s = stream if stream is not None else torch.cuda.current_stream(k_new.device)
-    ds = [_ref(describe(t)) for t in (q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache,
-                                      v_cache, k_scale, v_scale, q_out)]
-    rc = lib.pa_kv_append_q8(*ds[:5], 1 if interleaved else 0, *ds[5:12], int(P), ds[12],
-                             ctypes.c_void_p(s.cuda_stream))
-    if rc != 0:
-        raise PaError(rc, lib.pa_last_error().decode())
+    keep, ds = _pack((q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, k_scale,
+                      v_scale, q_out))
+    _call(lib.pa_kv_append_q8, k_new, stream, *ds[:5], 1 if interleaved else 0, *ds[5:12], int(P), ds[12])
     return q_out
 
 
@@ -319,6 +363,41 @@ def kv_append_q8_check(descriptors, page_block_size, interleaved=False) -> int:
     cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, k_scale, v_scale, q_out."""
     d = [_ref(x) for x in descriptors]
     return load().pa_kv_append_q8_check(*d[:5], 1 if interleaved else 0, *d[5:12], int(page_block_size), d[12])
+
+
+def varlen_fwd_q8(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_table, max_seqlen_q=None,
+                  max_seqlen_k=None, softmax_scale=None, window_left=-1, window_right=0, alibi_slopes=None, out=None,
+                  softmax_lse=None, page_block_size=None, stream=None) -> Tuple[object, object]:
+    """pa_varlen_fwd_q8 on torch CUDA tensors: :func:`varlen_fwd` over caches of
+    ``torch.float8_e4m3fn`` codes with the fp32 scales ``k_scale`` / ``v_scale`` (num_blocks,
+    num_heads_k) of every page and kv head; q and out are f16 or bf16.  Returns (out,
+    softmax_lse), allocated with torch when not given."""
+    import torch
+    lib = load()
+    if max_seqlen_q is None or max_seqlen_k is None:
+        raise ValueError("max_seqlen_q and max_seqlen_k are required")
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(q.shape[-1])
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if softmax_lse is None:
+        softmax_lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    P = page_block_size if page_block_size is not None else k_cache.shape[1]
+    keep, ds = _pack((q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_table, alibi_slopes, out,
+                      softmax_lse))
+    _call(lib.pa_varlen_fwd_q8, q, stream, *ds[:8], int(max_seqlen_q), int(max_seqlen_k), q.shape[-2],
+          k_cache.shape[-2], q.shape[-1], int(P), float(softmax_scale), int(window_left), int(window_right), *ds[8:])
+    return out, softmax_lse
+
+
+def varlen_check_q8(descriptors, max_seqlen_q, max_seqlen_k, num_heads, num_heads_k, head_dim, page_block_size,
+                    softmax_scale=0.125, window_left=-1, window_right=0) -> int:
+    """Host-only checks of pa_varlen_fwd_q8 on the descriptors (PaTensor or None) of q, k_cache, v_cache,
+    k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_table, alibi_slopes, out, softmax_lse."""
+    d = [_ref(x) for x in descriptors]
+    return load().pa_varlen_check_q8(*d[:8], int(max_seqlen_q), int(max_seqlen_k), int(num_heads), int(num_heads_k),
+                                     int(head_dim), int(page_block_size), float(softmax_scale), int(window_left),
+                                     int(window_right), *d[8:])
 
 
 def fwd_padded(q, k, v, softmax_scale=None, window_left=-1, window_right=0, alibi_slopes=None, out=None,

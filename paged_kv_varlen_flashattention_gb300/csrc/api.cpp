@@ -526,6 +526,37 @@ int q8_append_args(const pa_tensor* q, const pa_tensor* kn, const pa_tensor* vn,
     return validate_rope(q, kn, vn, cos, sin, q_out, true, check_device, a);
 }
 
+// The 16-bit checks on descriptors that stand for the caches, then what an 8-bit cache adds.
+int validate_q8(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, const pa_tensor* ks, const pa_tensor* vs,
+                const pa_tensor* cu_q, const pa_tensor* cu_k, const pa_tensor* bt, int32_t max_sq, int32_t max_sk,
+                int32_t num_heads, int32_t num_heads_k, int32_t head_dim, int32_t page_block_size, float softmax_scale,
+                int32_t wl, int32_t wr, const pa_tensor* alibi, const pa_tensor* out, const pa_tensor* lse,
+                bool check_device, pa::Args* a) {
+    if (!q || !k || !v || !ks || !vs || !bt)
+        return fail(PA_ERR_ARG, "a tensor descriptor is NULL (only alibi_slopes may be)");
+    const pa_tensor k16 = with_dtype(k, q->dtype), v16 = with_dtype(v, q->dtype);
+    int rc = validate(q, &k16, &v16, cu_q, cu_k, bt, max_sq, max_sk, num_heads, num_heads_k, head_dim, page_block_size,
+                      softmax_scale, wl, wr, alibi, out, lse, check_device, a);
+    if (rc != PA_OK) return rc;
+    if ((rc = check_q8_cache(k, v, ks, vs, check_device)) != PA_OK) return rc;
+    a->k_scale = static_cast<const float*>(ks->data);
+    a->v_scale = static_cast<const float*>(vs->data);
+    a->ks_s0 = ks->stride[0];
+    a->ks_s1 = ks->stride[1];
+    a->vs_s0 = vs->stride[0];
+    a->vs_s1 = vs->stride[1];
+    // the row tiles of sequences that no tensor-core prefill kernel takes, in grid.y
+    const int64_t rows = std::max<int64_t>(1, (int64_t)max_sq * (a->H / a->Hkv));
+    const int64_t row_tiles = rows <= 16 ? 1 : (rows + 31) / 32;
+    if ((int64_t)a->Hkv * row_tiles > 65535)
+        return fail(PA_ERR_UNSUPPORTED,
+                    "num_heads_k (%d) x row tiles of max_seqlen_q x group (%lld) exceeds 65535 CTAs per sequence; split "
+                    "the call into shorter query chunks",
+                    a->Hkv, (long long)row_tiles);
+    g_msg[0] = '\0';
+    return PA_OK;
+}
+
 // ---- per-(device, stream) split-KV workspace ------------------------------------------------
 std::mutex g_ws_mu;
 std::map<std::pair<int, cudaStream_t>, pa::Workspace> g_ws;
@@ -705,7 +736,7 @@ void timer_end(int cls, cudaStream_t stream) {
 }
 
 int encode_tmap_4d(void* map, int dtype, const void* base, const uint64_t dims_[4], const uint64_t strides_bytes[3],
-                   const uint32_t box[4], int swizzle128, char* msg, size_t msg_len) {
+                   const uint32_t box[4], int swizzle, char* msg, size_t msg_len) {
     auto fn = encode_fn();
     if (!fn) {
         snprintf(msg, msg_len, "cuTensorMapEncodeTiled is not available from the driver");
@@ -716,9 +747,14 @@ int encode_tmap_4d(void* map, int dtype, const void* base, const uint64_t dims_[
     cuuint32_t bdim[4] = {box[0], box[1], box[2], box[3]};
     cuuint32_t estride[4] = {1, 1, 1, 1};
     CUresult r = fn(reinterpret_cast<CUtensorMap*>(map),
-                    dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                    dtype == PA_E4M3   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                    : dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                    4,
                     const_cast<void*>(base), gdim, gstride, bdim, estride, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                    swizzle == 1   ? CU_TENSOR_MAP_SWIZZLE_128B
+                    : swizzle == 2 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                   : CU_TENSOR_MAP_SWIZZLE_NONE,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         snprintf(msg, msg_len,
@@ -832,8 +868,57 @@ SplitPlan plan_splitkv(const Args& a, bool prefill_takes_long_rows, int prefill_
     return pl;
 }
 
+SplitPlan plan_q8(const Args& a, bool prefill_takes_long_rows, int prefill_sms, int num_sms) {
+    SplitPlan pl{};
+    pl.dp = a.D <= 64 ? 64 : a.D <= 128 ? 128 : a.D <= 256 ? 256 : 512;
+    pl.nt = pl.dp == 512 ? 64 : 128;
+    const int G = a.H / a.Hkv;
+    const int64_t rows_max = (int64_t)a.max_sq * G;
+    pl.rows_cap = prefill_takes_long_rows ? prefill_rows_threshold() : (1 << 30);
+    const int64_t rows_here = std::max<int64_t>(1, std::min<int64_t>(rows_max, pl.rows_cap));
+    pl.mt = rows_here <= 16 ? 1 : 2;
+    const int M = 16 * pl.mt;
+    pl.row_tiles = (int)((rows_here + M - 1) / M);
+    pl.tile_rows = (int)std::min<int64_t>(M, rows_here);
+    int64_t kspan = a.max_sk;  // keys one row tile can touch: bounded by a window of two sides only
+    if (a.wl >= 0 && a.wr >= 0) kspan = std::min<int64_t>(kspan, (int64_t)a.wl + M / G + 1 + a.wr + 1);
+    const int64_t tiles_max = std::max<int64_t>(1, kspan / pl.nt + 2);
+    const int64_t units = (int64_t)a.batch * a.Hkv * pl.row_tiles;
+    pl.slots = num_sms * (a.dtype == PA_BF16 ? q8_occupancy_bf16(pl) : q8_occupancy_f16(pl));
+    // As the 16-bit plan: one wave of splits when there are fewer units than resident CTAs, one
+    // CTA per unit otherwise or beside a prefill grid that may take every SM; a split takes at
+    // least 256 keys and 16 per row (its fp32 partial, written and read, is then at most a
+    // quarter of the K/V bytes), and never more than the block ids and scales a CTA stages.
+    const int64_t slots = prefill_sms >= num_sms ? 0 : pl.slots;
+    int64_t splits = units < slots ? slots / units : 1;
+    splits = std::max<int64_t>(1, std::min(splits, tiles_max));
+    const int64_t min_tiles = std::max<int64_t>(256, 16ll * pl.tile_rows) / pl.nt;
+    int64_t split_tiles = std::max<int64_t>(min_tiles, (tiles_max + splits - 1) / splits);
+    const char* env_tiles = std::getenv("PA_SPLIT_TILES");
+    if (env_tiles) split_tiles = std::max<int64_t>(1, std::atoll(env_tiles));
+    split_tiles = std::min(split_tiles, std::min<int64_t>(kMaxSplitKeys / pl.nt, tiles_max));
+    pl.split_tiles = (int)split_tiles;
+    pl.max_splits = (int)std::min<int64_t>((tiles_max + split_tiles - 1) / split_tiles, INT32_MAX);
+    pl.work = pl.row_tiles == 1 && pl.dp <= 256 && a.batch >= kWorkMinBatch && a.batch <= kMaxOrderBatch &&
+              pl.max_splits > 1;
+    const bool one_wave = units * pl.max_splits <= pl.slots;
+    const bool ranked = !pl.work && !one_wave;
+    pl.rank_in_cta = ranked && a.batch >= 2 && a.batch <= kRankInCta;
+    pl.order_bytes = ranked && a.batch > kRankInCta && a.batch <= kMaxOrderBatch
+                         ? ((size_t)a.batch * sizeof(int) + 255) / 256 * 256
+                         : 0;
+    pl.work_bytes = pl.work ? ((2 + 2 * (size_t)a.batch * pl.max_splits) * sizeof(int) + 255) / 256 * 256 : 0;
+    pl.ws_bytes = pl.order_bytes + pl.work_bytes;
+    if (pl.max_splits > 1)
+        pl.ws_bytes += (size_t)pl.max_splits * (size_t)a.total_q * a.H * ((size_t)a.D + 1) * sizeof(float) + 256;
+    return pl;
+}
+
 int launch_splitkv(const Args& a, const SplitPlan& plan, void* workspace, unsigned int* err, char* msg,
                    size_t msg_len) {
+    if (a.k_scale)
+        return a.dtype == PA_BF16 ? launch_q8_bf16(a, plan, workspace, err, msg, msg_len)
+                                  : launch_q8_f16(a, plan, workspace, err, msg, msg_len);
     if (a.dtype == PA_BF16) return launch_splitkv_bf16(a, plan, workspace, err, msg, msg_len);
     return launch_splitkv_f16(a, plan, workspace, err, msg, msg_len);
 }
@@ -872,12 +957,16 @@ int launch_forward(pa::Args& a, void* stream, ScratchFn scratch, void* scratch_c
     int ce = pa::error_word(&err);
     if (ce != cudaSuccess) return fail(PA_ERR_CUDA, "error word: %s", cudaGetErrorString((cudaError_t)ce));
 
-    const bool use_prefill = pa::prefill_supported(a);
+    const bool use_prefill = a.k_scale ? false : pa::prefill_supported(a);
     // SMs the persistent prefill grid may hold beside the decode-class pass (it runs before
     // that pass, not beside it, when there is no side stream)
     const int prefill_sms =
         use_prefill && side_stream_ok ? (int)std::min<int64_t>(sm_count(), pa::prefill_items_bound(a)) : 0;
-    const pa::SplitPlan plan = pa::plan_splitkv(a, use_prefill, prefill_sms, sm_count());
+    const pa::SplitPlan plan = a.k_scale ? pa::plan_q8(a, use_prefill, prefill_sms, sm_count())
+                                         : pa::plan_splitkv(a, use_prefill, prefill_sms, sm_count());
+    if (plan.max_splits > 1024)  // only an 8-bit call's: its splits are bounded, and so is the combine
+        return fail(PA_ERR_UNSUPPORTED, "max_seqlen_k %d: an 8-bit cache call takes at most %d keys", a.max_sk,
+                    1000 * (int)pa::kMaxSplitKeys);
     // the prefill kernels' item counter follows the split-KV scratch
     const size_t counter_at = (plan.ws_bytes + 255) / 256 * 256;
     const size_t ws_bytes = use_prefill ? counter_at + pa::kPrefillCounterBytes : plan.ws_bytes;
@@ -1091,6 +1180,34 @@ int pa_kv_append(const pa_tensor* k_new, const pa_tensor* v_new, const pa_tensor
     rc = pa::launch_kv_append(a, err, g_msg, sizeof g_msg);
     if (rc == PA_OK) g_msg[0] = '\0';
     return rc;
+}
+
+// ---- attention over an 8-bit cache ----
+int pa_varlen_check_q8(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* k_scale,
+                       const pa_tensor* v_scale, const pa_tensor* cu_seqlens_q, const pa_tensor* cu_seqlens_k,
+                       const pa_tensor* block_table, int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads,
+                       int32_t num_heads_k, int32_t head_dim, int32_t page_block_size, float softmax_scale,
+                       int32_t window_left, int32_t window_right, const pa_tensor* alibi_slopes, const pa_tensor* out,
+                       const pa_tensor* softmax_lse) {
+    pa::Args a{};
+    return validate_q8(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_table, max_seqlen_q,
+                       max_seqlen_k, num_heads, num_heads_k, head_dim, page_block_size, softmax_scale, window_left,
+                       window_right, alibi_slopes, out, softmax_lse, false, &a);
+}
+
+int pa_varlen_fwd_q8(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* v_cache, const pa_tensor* k_scale,
+                     const pa_tensor* v_scale, const pa_tensor* cu_seqlens_q, const pa_tensor* cu_seqlens_k,
+                     const pa_tensor* block_table, int32_t max_seqlen_q, int32_t max_seqlen_k, int32_t num_heads,
+                     int32_t num_heads_k, int32_t head_dim, int32_t page_block_size, float softmax_scale,
+                     int32_t window_left, int32_t window_right, const pa_tensor* alibi_slopes, const pa_tensor* out,
+                     const pa_tensor* softmax_lse, void* stream) {
+    pa::NvtxRange range("pa_varlen_fwd_q8");
+    pa::Args a{};
+    const int rc = validate_q8(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_table,
+                               max_seqlen_q, max_seqlen_k, num_heads, num_heads_k, head_dim, page_block_size,
+                               softmax_scale, window_left, window_right, alibi_slopes, out, softmax_lse, true, &a);
+    if (rc != PA_OK) return rc;
+    return pa::launch_forward(a, stream, library_workspace, nullptr, true);
 }
 
 // ---- append with the position rotation, and into an 8-bit cache ----

@@ -120,6 +120,13 @@ bool decode_tc_wanted(int dp);
 int launch_splitkv_f16(const Args& a, const SplitPlan& plan, void* workspace, unsigned int* err, char* msg,
                        size_t msg_len);
 
+// The same over an 8-bit cache (Args::k_scale set): plan, kernels (q8_decode.cuh), and occupancy.
+SplitPlan plan_q8(const Args& a, bool prefill_takes_long_rows, int prefill_sms, int num_sms);
+int launch_q8_bf16(const Args& a, const SplitPlan& plan, void* workspace, unsigned int* err, char* msg, size_t msg_len);
+int launch_q8_f16(const Args& a, const SplitPlan& plan, void* workspace, unsigned int* err, char* msg, size_t msg_len);
+int q8_occupancy_bf16(const SplitPlan& plan);
+int q8_occupancy_f16(const SplitPlan& plan);
+
 // Device address (current device) of the library's error word, which kernels set
 // with the first PA_ERR_DEVICE_* code they meet (bit 31 = set).  Returns a cudaError_t.
 int error_word(unsigned int** ptr);
@@ -204,8 +211,9 @@ int forward_impl(const pa_tensor* q, const pa_tensor* k_cache, const pa_tensor* 
                  bool side_stream_ok);
 
 // Tensor-map encoding through the driver entry point (no libcuda link needed).
-// Rank-4 bf16/f16 map over (d0 fastest .. d3), strides in bytes for dims 1..3.
+// Rank-4 map of bf16/f16/e4m3 elements over (d0 fastest .. d3), strides in bytes for dims 1..3;
+// swizzle: 0 none, 1 128 bytes, 2 64 bytes.
 int encode_tmap_4d(void* map, int dtype, const void* base, const uint64_t dims[4], const uint64_t strides_bytes[3],
-                   const uint32_t box[4], int swizzle128, char* msg, size_t msg_len);
+                   const uint32_t box[4], int swizzle, char* msg, size_t msg_len);
 
 }  // namespace pa

@@ -1,0 +1,991 @@
+// Attention over an 8-bit paged cache (pa_varlen_fwd_q8): the split-KV kernels on mma.sync,
+// for decode-class rows and, tile by tile, for every call the tensor-core prefill kernel
+// does not take.
+//
+// K and V elements are e4m3 codes with one scale per page and kv head: K = ks Kc, V = vs Vc.
+// Neither is ever scaled element by element.  With c = softmax_scale log2(e) and a running
+// reference m, the softmax works on
+//     x_j = c ks_j (q . Kc_j) [- bias] + log2 vs_j,     w_j = 2^(x_j - m + 10),
+//     O = sum_j w_j Vc_j,     l = sum_j w_j / vs_j,     out = O / l,
+//     lse = (m - 10 + log2 l) ln 2,
+// which is softmax(s) V with the page's value scale moved into the exponent: O and its reference
+// live in units of V, so pages of very different magnitude keep their precision, and l takes
+// the scale back out, one multiplication per 16 keys.  m is the largest x so far; the offset of
+// 10 keeps weights down to 2^-24 of the largest in the normal range of f16 (2^-34 above zero).
+//
+// The codes become f16 on the way into the matrix instructions, where every e4m3 value is exact
+// (two elements an instruction; bf16 has no such conversion), and q and the weights are f16 beside
+// them: f16 q as it is; bf16 q times a power of two per row that brings the row's largest
+// magnitude to 2^14..2^15, taken back out in fp32 with the score's scale (bf16 has fewer
+// significant bits than f16, so only elements below 2^-28 of the row's largest lose any); the
+// weights rounded to 11 bits, where the 16-bit kernels of bf16 calls round them to 8.
+//
+// The column order inside a fragment is free as long as both operands share it, so a lane's
+// 4 bytes of a K row (one 32-bit ldmatrix element pair) are used as columns 4t..4t+3 without
+// any shuffle, and q is read to match.  V is loaded two columns at a time with ldmatrix.trans,
+// one byte permute per register puts the two keys of a column side by side, and even and odd
+// columns go to two accumulators, whose lanes hold four consecutive columns.
+//
+// HBM-bound: 2 bytes per (key, kv head, column).
+#pragma once
+
+#include "q8_common.cuh"
+#include "rope_common.cuh"
+#include "splitkv_kernel.cuh"
+
+namespace pa {
+
+struct Q8Params : SplitParams {
+    const float* ks;
+    const float* vs;
+    int64_t ks_s0, ks_s1, vs_s0, vs_s1;
+    int box_shift;  // log2(box_rows)
+};
+
+constexpr int kQ8MaxBoxes = 256;         // TMA boxes (32 rows or more) of one split
+constexpr int kQ8MaxSplitKeys = 8192;    // so that they suffice
+constexpr float kQ8Offset = 10.f;
+
+__device__ __forceinline__ bool q8_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
+                                        unsigned int* err, uint64_t limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (global_timer_ns() - t0 > limit_ns) {
+            *abort_flag = 1u;
+            flag_error(err, PA_ERR_DEVICE_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// log2 of a value scale; scales below 2^-100 (zero among them) are read as 2^-100.
+__device__ __forceinline__ float q8_log2_scale(float vs) {
+    return vs > 7.8886090522101181e-31f ? fminf(log2f(vs), 126.f) : (float)kScaleExpMin;
+}
+
+// Byte offset of 16-byte unit `u` of row `r` in a tile of rows of DP bytes as TMA leaves it:
+// 128-byte column chunks (chunk-major, NT rows each) under the 128-byte swizzle, or 64-byte rows
+// under the 64-byte swizzle (unit bits XOR address bits 7..8).
+template <int DP, int NT>
+__device__ __forceinline__ uint32_t q8_off(int r, int u) {
+    if constexpr (DP == 64)
+        return (uint32_t)(r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+    else
+        return (uint32_t)((u >> 3) * (NT * 128)) + swz128(r, u & 7);
+}
+
+// Rows' bounds and bias of a tile into shared memory; padding rows attend nothing.
+struct Q8Rows {
+    int* lo;
+    int* hi;
+    int* dg;
+    float* ab;
+    float* sc;  // score scale of the row: c / (power of two on its q)
+};
+__device__ __forceinline__ Q8Rows q8_rows(uint8_t* base, int M) {
+    int* p = reinterpret_cast<int*>(base);
+    return {p, p + M, p + 2 * M, reinterpret_cast<float*>(p + 3 * M), reinterpret_cast<float*>(p + 4 * M)};
+}
+__device__ __forceinline__ void q8_row_bounds(const SplitParams& p, const TileView& tv, const Q8Rows& rows, int hk,
+                                              int M) {
+    const int r = threadIdx.x;
+    if (r >= M) return;
+    int lo = 0, hi = -1, dg = 0;
+    float ab = 0.f;
+    if (r < tv.rows) {
+        const int64_t i = (tv.row0 + r) / p.G;
+        const int64_t diag = i + tv.sk - tv.sq;
+        lo = p.wl >= 0 ? (int)max64(0, diag - p.wl) : 0;
+        hi = p.wr >= 0 ? (int)max64(-1, min64(tv.sk - 1, diag + p.wr)) : tv.sk - 1;
+        dg = (int)diag;
+        if (p.alibi) ab = p.alibi[hk * p.G + (int)(tv.row0 + r - i * p.G)] * kLog2e;
+    }
+    rows.lo[r] = lo;
+    rows.hi[r] = hi;
+    rows.dg[r] = dg;
+    rows.ab[r] = ab;
+}
+
+// q rows as f16 into shared memory (row pitch `pitch` bytes, zero padded), warp w of NW taking
+// rows w, w + NW, ...; each row's power of two and score scale into rows.sc.
+template <typename T, int DP, int M, int NW>
+__device__ __forceinline__ void q8_stage_q(const SplitParams& p, const TileView& tv, const Q8Rows& rows, uint8_t* qs,
+                                           int pitch, int hk, int warp, int lane) {
+    constexpr int RPW = M / NW;
+    constexpr int UL = (DP / 8 + 31) / 32;  // 16-byte units a lane takes of a row
+    const T* q = static_cast<const T*>(p.q);
+    uint4 x[RPW][UL];
+#pragma unroll
+    for (int k = 0; k < RPW; ++k) {
+        const int r = warp + k * NW;
+        const int rho = tv.row0 + r, i = rho / p.G, g = rho - i * p.G;
+#pragma unroll
+        for (int c = 0; c < UL; ++c) {
+            const int u = lane + 32 * c;
+            x[k][c] = make_uint4(0, 0, 0, 0);
+            if (r < tv.rows && u * 8 < p.D)
+                x[k][c] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)(tv.q0 + i) * p.q_s0 +
+                                                               (int64_t)(hk * p.G + g) * p.q_s1 + u * 8));
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < RPW; ++k) {
+        const int r = warp + k * NW;
+        float sc = p.scale_log2;
+        if constexpr (!std::is_same<T, __half>::value) {
+            float v[UL][8], mx = 0.f;
+#pragma unroll
+            for (int c = 0; c < UL; ++c) {
+                const uint32_t w[4] = {x[k][c].x, x[k][c].y, x[k][c].z, x[k][c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = unpack2<T>(w[e]);
+                    v[c][2 * e] = f.x;
+                    v[c][2 * e + 1] = f.y;
+                    mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const int e2 = min(126, 14 - ((__float_as_int(mx) >> 23) - 127));
+            const float up = __int_as_float((127 + e2) << 23), down = __int_as_float((127 - e2) << 23);
+            sc *= down;
+#pragma unroll
+            for (int c = 0; c < UL; ++c)
+                x[k][c] = make_uint4(pack2<__half>(v[c][0] * up, v[c][1] * up), pack2<__half>(v[c][2] * up, v[c][3] * up),
+                                     pack2<__half>(v[c][4] * up, v[c][5] * up), pack2<__half>(v[c][6] * up, v[c][7] * up));
+        }
+        if (lane == 0) rows.sc[r] = sc;
+#pragma unroll
+        for (int c = 0; c < UL; ++c) {
+            const int u = lane + 32 * c;
+            if (u * 8 < DP) *reinterpret_cast<uint4*>(qs + r * pitch + u * 16) = x[k][c];
+        }
+    }
+}
+
+// One producer warp (K or V): the block ids of the split's boxes into `ids`, their scales (as
+// they are, or as log2 for V) into `sc`, the tiles into the ring.  Whole warp; lane 0 issues.
+template <int DP, int NT, int STAGES>
+__device__ __forceinline__ void q8_produce(const Q8Params& p, const CUtensorMap* map, uint8_t* ring, uint64_t* full,
+                                           uint64_t* empty, uint64_t* sc_full, int* ids, float* sc,
+                                           const float* scales, int64_t s0, int64_t s1, bool as_log2, int b, int hk,
+                                           int sk, int kbeg, int n_iter, int g0, volatile uint32_t* abort_flag) {
+    constexpr int CB = DP < 128 ? DP : 128, CH = DP / CB;
+    const int lane = threadIdx.x & 31;
+    const int32_t* bt_row = p.bt + (int64_t)b * p.bt_s0;
+    const int n_boxes = min(n_iter * p.boxes_per_tile, kQ8MaxBoxes);
+    float v[kQ8MaxBoxes / 32];
+#pragma unroll
+    for (int i = 0; i < kQ8MaxBoxes / 32; ++i) {
+        const int bi = lane + 32 * i;
+        v[i] = 0.f;
+        if (bi < n_boxes) {
+            const int blk = box_block(bt_row, p.bt_cols, p.num_blocks, p.P, kbeg + bi * p.box_rows, sk, p.err);
+            ids[bi] = blk;
+            if (blk >= 0) v[i] = __ldg(scales + (int64_t)blk * s0 + (int64_t)hk * s1);
+        }
+    }
+    __syncwarp();
+    const uint64_t policy = l2_policy_evict_first();
+    auto issue = [&](int it) -> bool {  // lane 0
+        const int gi = g0 + it, stage = gi % STAGES;
+        if (gi >= STAGES && !q8_wait(&empty[stage], ((gi / STAGES) - 1) & 1, abort_flag, p.err, p.wait_ns)) return false;
+        uint8_t* st = ring + stage * (NT * DP);
+        uint32_t bytes = 0;
+        for (int j = 0; j < p.boxes_per_tile; ++j)
+            if (ids[it * p.boxes_per_tile + j] >= 0) bytes += (uint32_t)(p.box_rows * DP);
+        mbar_arrive_expect_tx(&full[stage], bytes);
+        for (int j = 0; j < p.boxes_per_tile; ++j) {
+            const int blk = ids[it * p.boxes_per_tile + j];
+            if (blk < 0) continue;
+            const int key = kbeg + it * NT + j * p.box_rows;
+            const int slot = key - (key / p.P) * p.P;
+#pragma unroll
+            for (int c = 0; c < CH; ++c)
+                tma_load_4d(st + c * (NT * CB) + j * p.box_rows * CB, map, &full[stage], c * CB, hk, slot, blk, policy);
+        }
+        return true;
+    };
+    bool ok = true;
+    int it = 0;
+    if (lane == 0 && !p.withhold)
+        for (; ok && it < min(STAGES, n_iter); ++it) ok = issue(it);
+    // the scales, whose loads ran beside the first copies
+#pragma unroll
+    for (int i = 0; i < kQ8MaxBoxes / 32; ++i) {
+        const int bi = lane + 32 * i;
+        if (bi < n_boxes) sc[bi] = as_log2 ? q8_log2_scale(v[i]) : v[i];
+    }
+    __syncwarp();
+    if (lane == 0) {
+        mbar_arrive(sc_full);
+        if (!p.withhold)
+            for (; ok && it < n_iter; ++it) ok = issue(it);
+    }
+}
+
+// Score of a (row, key): masked by select, biased, in units of V (lv = log2 of its scale).
+__device__ __forceinline__ float q8_score(float s, float c, float lv, bool in, float ab, int dg, int key) {
+    return in ? fmaf(-ab, fabsf((float)(dg - key)), fmaf(s, c, lv)) : -INFINITY;
+}
+
+// ---------------------------------------------------------------------------------------------
+// decode_q8_kernel: head_dim <= 256, NW consumer warps with private key slices of every tile
+// (as decode_kernel), one producer warp for K and one for V.
+template <int DP_, int MG, int NW, int NT, int STAGES, int ML = MG>
+struct Q8Cfg {
+    static constexpr int DP = DP_;
+    static constexpr int M = 16 * MG;
+    static constexpr int KW = NW / MG;   // warps sharing a row group
+    static constexpr int KPW = NT / KW;  // keys per warp and tile
+    static constexpr int CK = DP <= 128 ? 2 : 1;  // 16-key chunks whose scores are in registers together
+    static constexpr int TILE = NT * DP;
+    static constexpr int QP = DP * 2 + 32;  // q row pitch: the four rows of a load phase in different banks
+    static constexpr int OFF_V = STAGES * TILE;
+    static constexpr int OFF_Q = 2 * STAGES * TILE;
+    static constexpr int OFF_ROW = OFF_Q + 16 * ML * QP;
+    static constexpr int OFF_BAR = (OFF_ROW + 5 * 16 * ML * 4 + 15) & ~15;  // k_full, k_empty, v_full, v_empty, sc_full
+    static constexpr int OFF_FLAG = OFF_BAR + (4 * STAGES + 1) * 8;
+    static constexpr int OFF_SC = (OFF_FLAG + 4 + 15) & ~15;  // K scales, log2 V scales
+    static constexpr int OFF_IDS = OFF_SC + 2 * kQ8MaxBoxes * 4;
+    static constexpr int SMEM = OFF_IDS + 2 * kQ8MaxBoxes * 4 + 1024;
+    static constexpr int THREADS = NW * 32 + 64;
+    static constexpr bool Q_IN_REGS = DP <= 128;
+    static constexpr int MERGE = NW * (DP / 8) * 32 * 16 + NW * 32 * 16;
+    static_assert(KPW % (16 * CK) == 0, "keys per warp");
+    static_assert((DP / 16) % KW == 0, "columns per warp in the merge");
+    static_assert(MERGE <= 2 * STAGES * TILE, "merge scratch");
+    static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+
+// One (sequence, kv head, row tile, split) on a CTA.  Returns whether there was work (uniform):
+// then sc_full went through one phase and the rings through n_done tiles.
+template <typename T, int DP, int MG, int NW, int NT, int STAGES, int ML>
+__device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Q8Params& p,
+                                               uint8_t* smem, int b, int hk, int rt, int split, int g0, int unit,
+                                               int& n_done) {
+    using C = Q8Cfg<DP, MG, NW, NT, STAGES, ML>;
+    constexpr int M = C::M;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    TileView tv;
+    n_done = 0;
+    if (!tile_view<M, NT>(p, b, rt, tv, split == 0)) return false;
+    if (split >= max(tv.nsplit, 1)) return false;
+    const bool single = tv.nsplit <= 1;
+    const int t_begin = split * p.split_tiles;
+    const int n_iter = max(0, min(tv.ntiles, t_begin + p.split_tiles) - t_begin);
+    n_done = n_iter;
+    const int kbeg = tv.kt0 + t_begin * NT;
+
+    const Q8Rows rows = q8_rows(smem + C::OFF_ROW, M);
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* k_empty = k_full + STAGES;
+    uint64_t* v_full = k_empty + STAGES;
+    uint64_t* v_empty = v_full + STAGES;
+    uint64_t* sc_full = v_empty + STAGES;
+    volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG);
+    float* ksc = reinterpret_cast<float*>(smem + C::OFF_SC);
+    float* lvs = ksc + kQ8MaxBoxes;
+    q8_row_bounds(p, tv, rows, hk, M);
+    __syncthreads();  // rows, and for a CTA's first unit the barriers
+
+    if (warp >= NW) {
+        int* ids = reinterpret_cast<int*>(smem + C::OFF_IDS);
+        if (warp == NW)
+            q8_produce<DP, NT, STAGES>(p, &tm_k, smem, k_full, k_empty, sc_full, ids, ksc, p.ks, p.ks_s0, p.ks_s1, false,
+                                       b, hk, tv.sk, kbeg, n_iter, g0, abort_flag);
+        else
+            q8_produce<DP, NT, STAGES>(p, &tm_v, smem + C::OFF_V, v_full, v_empty, sc_full, ids + kQ8MaxBoxes, lvs, p.vs,
+                                       p.vs_s0, p.vs_s1, true, b, hk, tv.sk, kbeg, n_iter, g0, abort_flag);
+        return true;
+    }
+    q8_stage_q<T, DP, M, NW>(p, tv, rows, smem + C::OFF_Q, C::QP, hk, warp, lane);
+    named_barrier_sync(1, NW * 32);
+
+    const int rg = warp / C::KW, kq = warp % C::KW;
+    const int gq = lane >> 2, tq = lane & 3;
+    const int mi = lane >> 3, rr = lane & 7;
+    const int r0 = rg * 16 + gq, r1 = r0 + 8;
+    const int lo0 = rows.lo[r0], hi0 = rows.hi[r0], lo1 = rows.lo[r1], hi1 = rows.hi[r1];
+    const int dg0 = rows.dg[r0], dg1 = rows.dg[r1];
+    const float ab0 = rows.ab[r0], ab1 = rows.ab[r1];
+    const float c0 = rows.sc[r0], c1 = rows.sc[r1];
+    const uint8_t* q0p = smem + C::OFF_Q + r0 * C::QP + tq * 8;
+    const uint8_t* q1p = smem + C::OFF_Q + r1 * C::QP + tq * 8;
+    // A fragment of k-step ks: columns 16 ks + 4 tq + {0, 1} and + {2, 3} of rows r0 and r1
+    auto q_frag = [&](int ks, uint32_t (&a)[4]) {
+        const uint2 x = *reinterpret_cast<const uint2*>(q0p + ks * 32), y = *reinterpret_cast<const uint2*>(q1p + ks * 32);
+        a[0] = x.x;
+        a[1] = y.x;
+        a[2] = x.y;
+        a[3] = y.y;
+    };
+    uint32_t qf[C::Q_IN_REGS ? DP / 16 : 1][4];
+    if constexpr (C::Q_IN_REGS) {
+#pragma unroll
+        for (int ks = 0; ks < DP / 16; ++ks) q_frag(ks, qf[ks]);
+    }
+    float o[DP / 8][4];  // [2 x unit + column parity]
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    bool ok = __all_sync(0xffffffffu, q8_wait(sc_full, unit & 1, abort_flag, p.err, p.wait_ns));
+
+    for (int it = 0; ok && it < n_iter; ++it) {
+        const int gi = g0 + it, stage = gi % STAGES;
+        const uint32_t par = (gi / STAGES) & 1;
+        const int kt = kbeg + it * NT;
+        const int key0 = kq * C::KPW;
+        const uint32_t k_base = smem_addr(smem + stage * C::TILE), v_base = smem_addr(smem + C::OFF_V + stage * C::TILE);
+        // V rows of this warp's slice that no row of the tile attends become 0 (0 x NaN is NaN):
+        // keys before the first interval, past the last, and slots that were never loaded
+        const int z_lo = min(max(tv.lo - kt, key0), key0 + C::KPW), z_hi = min(max(tv.hi + 1 - kt, key0), key0 + C::KPW);
+        const bool zeroed = z_lo > key0 || z_hi < key0 + C::KPW;
+        ok = __all_sync(0xffffffffu, q8_wait(&k_full[stage], par, abort_flag, p.err, p.wait_ns));
+        if (!ok) break;
+#pragma unroll
+        for (int kb = 0; kb < C::KPW / (16 * C::CK); ++kb) {
+            float s[C::CK][2][4];
+#pragma unroll
+            for (int kc = 0; kc < C::CK; ++kc) {
+                const int kk0 = key0 + (kb * C::CK + kc) * 16;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[kc][n][e] = 0.f;
+#pragma unroll
+                for (int kp = 0; kp < DP / 32; ++kp) {
+                    uint32_t b0, b1, b2, b3;  // (keys 0..7, k-step 2 kp), (same, 2 kp + 1), (keys 8..15, ...)
+                    ldsm_x4(k_base + q8_off<DP, NT>(kk0 + rr + ((mi >> 1) << 3), 2 * kp + (mi & 1)), b0, b1, b2, b3);
+                    uint32_t a0[4], a1[4];
+                    if constexpr (C::Q_IN_REGS) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            a0[e] = qf[2 * kp][e];
+                            a1[e] = qf[2 * kp + 1][e];
+                        }
+                    } else {
+                        q_frag(2 * kp, a0);
+                        q_frag(2 * kp + 1, a1);
+                    }
+                    MmaOp<__half>::run(s[kc][0], a0, e4m3x2_to_half2(b0), e4m3x2_hi_to_half2(b0));
+                    MmaOp<__half>::run(s[kc][1], a0, e4m3x2_to_half2(b2), e4m3x2_hi_to_half2(b2));
+                    MmaOp<__half>::run(s[kc][0], a1, e4m3x2_to_half2(b1), e4m3x2_hi_to_half2(b1));
+                    MmaOp<__half>::run(s[kc][1], a1, e4m3x2_to_half2(b3), e4m3x2_hi_to_half2(b3));
+                }
+            }
+            if (kb + 1 == C::KPW / (16 * C::CK)) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&k_empty[stage]);
+            }
+            // scores, row maxima, weights
+            float mx0 = -INFINITY, mx1 = -INFINITY;
+            float inv[C::CK];
+#pragma unroll
+            for (int kc = 0; kc < C::CK; ++kc) {
+                const int kk0 = key0 + (kb * C::CK + kc) * 16;
+                const int box = (it * NT + kk0) >> p.box_shift;  // a chunk of 16 keys lies in one page
+                const float kss = ksc[box], lv = lvs[box];
+                inv[kc] = exp2f(-lv);
+                const float k0 = c0 * kss, k1 = c1 * kss;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = kt + kk0 + n * 8 + tq * 2 + (e & 1);
+                        float& x = s[kc][n][e];
+                        if (e < 2) {
+                            x = q8_score(x, k0, lv, key >= lo0 && key <= hi0, ab0, dg0, key);
+                            mx0 = fmaxf(mx0, x);
+                        } else {
+                            x = q8_score(x, k1, lv, key >= lo1 && key <= hi1, ab1, dg1, key);
+                            mx1 = fmaxf(mx1, x);
+                        }
+                    }
+            }
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+            const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+            if (__any_sync(0xffffffffu, n0 > m0 || n1 > m1)) {
+                const float f0 = n0 == -INFINITY ? 1.f : fast_exp2(m0 - n0);
+                const float f1 = n1 == -INFINITY ? 1.f : fast_exp2(m1 - n1);
+#pragma unroll
+                for (int n = 0; n < DP / 8; ++n) {
+                    o[n][0] *= f0;
+                    o[n][1] *= f0;
+                    o[n][2] *= f1;
+                    o[n][3] *= f1;
+                }
+                l0 *= f0;
+                l1 *= f1;
+                m0 = n0;
+                m1 = n1;
+            }
+            const float u0 = m0 == -INFINITY ? 0.f : m0 - kQ8Offset, u1 = m1 == -INFINITY ? 0.f : m1 - kQ8Offset;
+            uint32_t pa[C::CK][4];
+#pragma unroll
+            for (int kc = 0; kc < C::CK; ++kc) {
+                float w[2][4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    w[n][0] = fast_exp2(s[kc][n][0] - u0);
+                    w[n][1] = fast_exp2(s[kc][n][1] - u0);
+                    w[n][2] = fast_exp2(s[kc][n][2] - u1);
+                    w[n][3] = fast_exp2(s[kc][n][3] - u1);
+                }
+                l0 = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), inv[kc], l0);
+                l1 = fmaf((w[0][2] + w[0][3]) + (w[1][2] + w[1][3]), inv[kc], l1);
+                pa[kc][0] = pack2<__half>(w[0][0], w[0][1]);
+                pa[kc][1] = pack2<__half>(w[0][2], w[0][3]);
+                pa[kc][2] = pack2<__half>(w[1][0], w[1][1]);
+                pa[kc][3] = pack2<__half>(w[1][2], w[1][3]);
+            }
+            if (kb == 0) {
+                ok = __all_sync(0xffffffffu, q8_wait(&v_full[stage], par, abort_flag, p.err, p.wait_ns));
+                if (!ok) break;
+                if (zeroed) {
+                    uint8_t* vst = smem + C::OFF_V + stage * C::TILE;
+                    for (int idx = lane; idx < C::KPW * (DP / 16); idx += 32) {
+                        const int r = key0 + idx / (DP / 16), u = idx % (DP / 16);
+                        if (r < z_lo || r >= z_hi)
+                            *reinterpret_cast<uint4*>(vst + q8_off<DP, NT>(r, u)) = make_uint4(0, 0, 0, 0);
+                    }
+                    __syncwarp();
+                }
+            }
+#pragma unroll
+            for (int kc = 0; kc < C::CK; ++kc) {
+                const int kk0 = key0 + (kb * C::CK + kc) * 16;
+#pragma unroll
+                for (int np = 0; np < DP / 32; ++np) {
+                    uint32_t v[4];  // (keys 0..7, unit 2 np), (keys 8..15, same), (keys 0..7, unit 2 np + 1), ...
+                    ldsm_x4_t(v_base + q8_off<DP, NT>(kk0 + rr + ((mi & 1) << 3), 2 * np + (mi >> 1)), v[0], v[1], v[2],
+                              v[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = __byte_perm(v[e], 0, 0x3120);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        MmaOp<__half>::run(o[2 * (2 * np + j)], pa[kc], e4m3x2_to_half2(v[2 * j]),
+                                           e4m3x2_to_half2(v[2 * j + 1]));
+                        MmaOp<__half>::run(o[2 * (2 * np + j) + 1], pa[kc], e4m3x2_hi_to_half2(v[2 * j]),
+                                           e4m3x2_hi_to_half2(v[2 * j + 1]));
+                    }
+                }
+            }
+        }
+        if (!ok) break;
+        if (zeroed) fence_proxy_async_smem();  // the stage is rewritten by TMA later
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_empty[stage]);
+    }
+
+    // ---- merge the key slices of each row group, each warp a share of the columns ----
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (named_barrier_or(1, NW * 32, !ok || *abort_flag != 0u)) return true;  // all leave together
+    float4* xo = reinterpret_cast<float4*>(smem);  // [warp][n][lane], in the rings
+    float4* xml = xo + NW * (DP / 8) * 32;         // [warp][lane]: m0, m1, l0, l1
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) xo[(warp * (DP / 8) + n) * 32 + lane] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+    xml[warp * 32 + lane] = make_float4(m0, m1, l0, l1);
+    named_barrier_sync(1, NW * 32);
+    float f0[C::KW], f1[C::KW];
+    float L0 = 0.f, L1 = 0.f, mm0 = -INFINITY, mm1 = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < C::KW; ++k) {
+        const float4 ml = xml[(rg * C::KW + k) * 32 + lane];
+        mm0 = fmaxf(mm0, ml.x);
+        mm1 = fmaxf(mm1, ml.y);
+    }
+    const float w0 = mm0 == -INFINITY ? 0.f : mm0, w1 = mm1 == -INFINITY ? 0.f : mm1;
+#pragma unroll
+    for (int k = 0; k < C::KW; ++k) {
+        const float4 ml = xml[(rg * C::KW + k) * 32 + lane];
+        f0[k] = fast_exp2(ml.x - w0);
+        f1[k] = fast_exp2(ml.y - w1);
+        L0 += f0[k] * ml.z;
+        L1 += f1[k] * ml.w;
+    }
+    const float inv0 = L0 == 0.f ? 0.f : 1.f / L0, inv1 = L1 == 0.f ? 0.f : 1.f / L1;
+    constexpr int UPW = (DP / 16) / C::KW;  // 16-column units this warp stores
+    T* out = static_cast<T*>(p.out);
+#pragma unroll
+    for (int hr = 0; hr < 2; ++hr) {
+        const int row = hr ? r1 : r0;
+        if (row >= tv.rows) continue;
+        const int rho = tv.row0 + row;
+        const int i = rho / p.G, g = rho - i * p.G;
+        const int64_t t = tv.q0 + i;
+        const int h = hk * p.G + g;
+        const float iv = hr ? inv1 : inv0;
+#pragma unroll
+        for (int uu = 0; uu < UPW; ++uu) {
+            const int u = kq * UPW + uu, d = u * 16 + tq * 4;
+            if (d >= p.D) continue;
+            float x[4] = {0.f, 0.f, 0.f, 0.f};  // columns d .. d + 3: even, odd, even, odd
+#pragma unroll
+            for (int k = 0; k < C::KW; ++k) {
+                const float4 ev = xo[((rg * C::KW + k) * (DP / 8) + 2 * u) * 32 + lane];
+                const float4 od = xo[((rg * C::KW + k) * (DP / 8) + 2 * u + 1) * 32 + lane];
+                const float f = hr ? f1[k] : f0[k];
+                x[0] += f * (hr ? ev.z : ev.x);
+                x[1] += f * (hr ? od.z : od.x);
+                x[2] += f * (hr ? ev.w : ev.y);
+                x[3] += f * (hr ? od.w : od.y);
+            }
+            if (single)
+                *reinterpret_cast<uint2*>(out + t * p.o_s0 + (int64_t)h * p.o_s1 + d) =
+                    make_uint2(pack2<T>(x[0] * iv, x[1] * iv), pack2<T>(x[2] * iv, x[3] * iv));
+            else
+                *reinterpret_cast<float4*>(p.part_o + ((int64_t)split * p.part_stride + t * p.H + h) * p.D + d) =
+                    make_float4(x[0] * iv, x[1] * iv, x[2] * iv, x[3] * iv);
+        }
+        if (kq == 0 && tq == 0) {
+            const float L = hr ? L1 : L0, mm = hr ? mm1 : mm0;
+            const float lse = L == 0.f ? -INFINITY : (mm - kQ8Offset + log2f(L)) * 0.69314718055994531f;
+            if (single)
+                p.lse[(int64_t)h * p.lse_s0 + t + (int64_t)b * p.lse_sb] = lse;
+            else
+                p.part_lse[(int64_t)split * p.part_stride + t * p.H + h] = lse;
+        }
+    }
+    return true;
+}
+
+// The sequence of a grid index: longest first (order from a ranking pass, or ranked here).
+__device__ __forceinline__ int q8_sequence(const SplitParams& p, int* rank_len, int* rank_pick) {
+    const int z = (int)blockIdx.z, tid = threadIdx.x;
+    if (p.order) return p.order[z];
+    if (!p.rank_in_cta) return z;
+    if (tid < p.batch) rank_len[tid] = p.cu_k[tid + 1] - p.cu_k[tid];
+    if (tid == 0) *rank_pick = z;
+    __syncthreads();
+    if (tid < p.batch) {
+        const int ls = rank_len[tid];
+        int rank = 0;
+        for (int t = 0; t < p.batch; ++t) {
+            const int lt = rank_len[t];
+            rank += (lt > ls) || (lt == ls && t < tid);
+        }
+        if (rank == z) *rank_pick = tid;
+    }
+    __syncthreads();
+    return *rank_pick;
+}
+
+template <typename T, int DP, int MG, int NW, int NT, int STAGES>
+__global__ void __launch_bounds__(NW * 32 + 64, DP <= 128 ? 2 : 1)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const Q8Params p) {
+    using C = Q8Cfg<DP, MG, NW, NT, STAGES>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x;
+    allow_dependent_launch();
+    if (tid == NW * 32) prefetch_tmap(&tm_k);
+    if (tid == NW * 32 + 32) prefetch_tmap(&tm_v);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG);
+    if (tid == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&bars[s], 1);                // k_full
+            mbar_init(&bars[STAGES + s], NW);      // k_empty
+            mbar_init(&bars[2 * STAGES + s], 1);   // v_full
+            mbar_init(&bars[3 * STAGES + s], NW);  // v_empty
+        }
+        mbar_init(&bars[4 * STAGES], 2);
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    // A kernel for two row groups runs a sequence of at most 16 rows on the one-group body.
+    auto run_unit = [&](int b, int hk, int rt, int split, int g0, int unit, int& n_done) -> bool {
+        if constexpr (MG == 2) {
+            using L1 = Q8Cfg<DP, 1, NW, NT, STAGES, 2>;
+            static_assert(L1::OFF_ROW == C::OFF_ROW && L1::OFF_BAR == C::OFF_BAR && L1::OFF_SC == C::OFF_SC &&
+                              L1::SMEM == C::SMEM,
+                          "both bodies share one shared-memory layout");
+            if (b >= 0 && b < p.batch && (int64_t)(p.cu_q[b + 1] - p.cu_q[b]) * p.G <= 16)
+                return decode_q8_unit<T, DP, 1, NW, NT, STAGES, 2>(tm_k, tm_v, p, smem, b, hk, rt, split, g0, unit, n_done);
+        }
+        return decode_q8_unit<T, DP, MG, NW, NT, STAGES, MG>(tm_k, tm_v, p, smem, b, hk, rt, split, g0, unit, n_done);
+    };
+    if (p.work) {  // persistent: (sequence, split) x kv head items in list order
+        __shared__ int s_item;
+        const int total = p.work[1] * p.Hkv;
+        int g0 = 0, unit = 0;
+        for (;;) {
+            if (tid == 0) s_item = atomicAdd(p.work, 1);
+            __syncthreads();
+            const int w = s_item;
+            if (w >= total) break;
+            const int pair = w / p.Hkv;
+            int n_done = 0;
+            const bool ran = run_unit(p.work[2 + 2 * pair], w - pair * p.Hkv, 0, p.work[3 + 2 * pair], g0, unit, n_done);
+            fence_proxy_async_smem();  // the merge's writes come before the next item's copies
+            __syncthreads();
+            if (*abort_flag) break;
+            g0 += n_done;
+            unit += ran ? 1 : 0;
+        }
+        return;
+    }
+    __shared__ int rank_len[kRankInCta];
+    __shared__ int rank_pick;
+    const int b = q8_sequence(p, rank_len, &rank_pick);
+    if (tid >= NW * 32 && tid < NW * 32 + 32) prefetch_split_pages<NT>(p, b, (int)blockIdx.x, tid - NW * 32);
+    int n_done = 0;
+    run_unit(b, (int)blockIdx.y % p.Hkv, (int)blockIdx.y / p.Hkv, (int)blockIdx.x, 0, 0, n_done);
+}
+
+// ---------------------------------------------------------------------------------------------
+// decode512_q8_kernel: head_dim 257..512.
+//
+// One warp cannot hold 16 rows x 512 columns of O.  Eight warps take key slices of a 64-key tile
+// for Q.K^T (8 keys each of all 16 rows, or 16 keys of one of two row groups), write their
+// weights to shared memory, and after one barrier take 64-column slices for P.V, all keys and
+// both row groups, so V is converted once.  The warps share one reference m per row: a tile whose
+// scores all lie below m + 5 needs no exchange (weights up to 2^15 fit f16); otherwise, a vote
+// folded into that barrier, they exchange row maxima, rescale and write the weights again.  The
+// weights are double-buffered, so the common tile costs one barrier.
+template <int MG>
+struct Q8WideCfg {
+    static constexpr int DP = 512, NW = 8, NT = 64, M = 16 * MG;
+    static constexpr int KST = 3, VST = MG == 1 ? 3 : 2;
+    static constexpr int KS = NW / MG;      // key slices
+    static constexpr int NB = NT / KS / 8;  // 8-key tiles per warp
+    static constexpr int TILE = NT * DP;
+    static constexpr int QP = DP * 2 + 32;
+    static constexpr int OFF_V = KST * TILE;
+    static constexpr int OFF_P = OFF_V + VST * TILE;         // weights, two buffers of M rows x 128 bytes
+    static constexpr int OFF_Q = OFF_P + 2 * M * 128;
+    static constexpr int OFF_ROW = OFF_Q + M * QP;
+    static constexpr int OFF_MAX = OFF_ROW + 5 * M * 4;      // [key slice][row]: maxima, then sums
+    static constexpr int OFF_BAR = (OFF_MAX + KS * M * 4 + 15) & ~15;
+    static constexpr int OFF_FLAG = OFF_BAR + (2 * KST + 2 * VST + 1) * 8;
+    static constexpr int OFF_SC = (OFF_FLAG + 4 + 15) & ~15;
+    static constexpr int OFF_IDS = OFF_SC + 2 * kQ8MaxBoxes * 4;
+    static constexpr int SMEM = OFF_IDS + 2 * kQ8MaxBoxes * 4 + 1024;
+    static constexpr int THREADS = NW * 32 + 64;
+    static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+};
+
+template <typename T, int MG>
+__global__ void __launch_bounds__(Q8WideCfg<MG>::THREADS, 1)
+    decode512_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const Q8Params p) {
+    using C = Q8WideCfg<MG>;
+    constexpr int DP = C::DP, NT = C::NT, NW = C::NW, M = C::M, NB = C::NB;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    allow_dependent_launch();
+    if (tid == NW * 32) prefetch_tmap(&tm_k);
+    if (tid == NW * 32 + 32) prefetch_tmap(&tm_v);
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* k_empty = k_full + C::KST;
+    uint64_t* v_full = k_empty + C::KST;
+    uint64_t* v_empty = v_full + C::VST;
+    uint64_t* sc_full = v_empty + C::VST;
+    volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG);
+    if (tid == 0) {
+        for (int s = 0; s < C::KST; ++s) {
+            mbar_init(&k_full[s], 1);
+            mbar_init(&k_empty[s], NW);
+        }
+        for (int s = 0; s < C::VST; ++s) {
+            mbar_init(&v_full[s], 1);
+            mbar_init(&v_empty[s], NW);
+        }
+        mbar_init(sc_full, 2);
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    __shared__ int rank_len[kRankInCta];
+    __shared__ int rank_pick;
+    const int b = q8_sequence(p, rank_len, &rank_pick);
+    const int hk = (int)blockIdx.y % p.Hkv, rt = (int)blockIdx.y / p.Hkv, split = (int)blockIdx.x;
+    TileView tv;
+    if (!tile_view<M, NT>(p, b, rt, tv, split == 0)) return;
+    if (split >= max(tv.nsplit, 1)) return;
+    const bool single = tv.nsplit <= 1;
+    const int t_begin = split * p.split_tiles;
+    const int n_iter = max(0, min(tv.ntiles, t_begin + p.split_tiles) - t_begin);
+    const int kbeg = tv.kt0 + t_begin * NT;
+    const Q8Rows rows = q8_rows(smem + C::OFF_ROW, M);
+    float* ksc = reinterpret_cast<float*>(smem + C::OFF_SC);
+    float* lvs = ksc + kQ8MaxBoxes;
+    float* xmax = reinterpret_cast<float*>(smem + C::OFF_MAX);
+    q8_row_bounds(p, tv, rows, hk, M);
+    __syncthreads();
+    if (warp >= NW) {
+        int* ids = reinterpret_cast<int*>(smem + C::OFF_IDS);
+        if (warp == NW)
+            q8_produce<DP, NT, C::KST>(p, &tm_k, smem, k_full, k_empty, sc_full, ids, ksc, p.ks, p.ks_s0, p.ks_s1, false,
+                                       b, hk, tv.sk, kbeg, n_iter, 0, abort_flag);
+        else
+            q8_produce<DP, NT, C::VST>(p, &tm_v, smem + C::OFF_V, v_full, v_empty, sc_full, ids + kQ8MaxBoxes, lvs, p.vs,
+                                       p.vs_s0, p.vs_s1, true, b, hk, tv.sk, kbeg, n_iter, 0, abort_flag);
+        return;
+    }
+    q8_stage_q<T, DP, M, NW>(p, tv, rows, smem + C::OFF_Q, C::QP, hk, warp, lane);
+    named_barrier_sync(1, NW * 32);
+
+    const int rg = warp / C::KS, slice = warp % C::KS;
+    const int gq = lane >> 2, tq = lane & 3;
+    const int mi = lane >> 3, rr = lane & 7;
+    const int r0 = rg * 16 + gq, r1 = r0 + 8;  // this warp's rows in Q.K^T
+    const int key0 = slice * NB * 8;
+    const int lo0 = rows.lo[r0], hi0 = rows.hi[r0], lo1 = rows.lo[r1], hi1 = rows.hi[r1];
+    const int dg0 = rows.dg[r0], dg1 = rows.dg[r1];
+    const float ab0 = rows.ab[r0], ab1 = rows.ab[r1];
+    const float c0 = rows.sc[r0], c1 = rows.sc[r1];
+    const uint8_t* q0p = smem + C::OFF_Q + r0 * C::QP + tq * 8;
+    const uint8_t* q1p = smem + C::OFF_Q + r1 * C::QP + tq * 8;
+    auto q_frag = [&](int ks, uint32_t (&a)[4]) {
+        const uint2 x = *reinterpret_cast<const uint2*>(q0p + ks * 32), y = *reinterpret_cast<const uint2*>(q1p + ks * 32);
+        a[0] = x.x;
+        a[1] = y.x;
+        a[2] = x.y;
+        a[3] = y.y;
+    };
+    float o[MG][8][4];  // [row group][2 x unit + parity]: columns 64 warp + 16 unit + 4 tq + ...
+    float m[MG][2];     // references of rows 16 g + gq and + 8
+#pragma unroll
+    for (int g = 0; g < MG; ++g) {
+        m[g][0] = m[g][1] = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[g][n][e] = 0.f;
+    }
+    auto mine = [&](int q) { return MG == 2 && rg ? m[MG - 1][q] : m[0][q]; };  // of this warp's Q.K^T rows
+    float l0 = 0.f, l1 = 0.f;  // sums of this warp's rows over its keys
+    bool ok = __all_sync(0xffffffffu, q8_wait(sc_full, 0, abort_flag, p.err, p.wait_ns));
+
+    for (int it = 0; it < n_iter; ++it) {
+        const int kst = it % C::KST, vst = it % C::VST;
+        const int kt = kbeg + it * NT;
+        if (ok) ok = __all_sync(0xffffffffu, q8_wait(&k_full[kst], (it / C::KST) & 1, abort_flag, p.err, p.wait_ns));
+        const uint32_t k_base = smem_addr(smem + kst * C::TILE), v_base = smem_addr(smem + C::OFF_V + vst * C::TILE);
+        float s[2][NB][4];  // two chains of products each
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[ch][n][e] = 0.f;
+        if (ok) {
+            if constexpr (NB == 1) {
+#pragma unroll
+                for (int kp = 0; kp < DP / 64; ++kp) {
+                    uint32_t bq[4];  // k-steps 4 kp .. 4 kp + 3 of the eight keys
+                    ldsm_x4(k_base + q8_off<DP, NT>(key0 + rr, 4 * kp + mi), bq[0], bq[1], bq[2], bq[3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t a[4];
+                        q_frag(4 * kp + j, a);
+                        MmaOp<__half>::run(s[j & 1][0], a, e4m3x2_to_half2(bq[j]), e4m3x2_hi_to_half2(bq[j]));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int kp = 0; kp < DP / 32; ++kp) {
+                    uint32_t bq[4];
+                    ldsm_x4(k_base + q8_off<DP, NT>(key0 + rr + ((mi >> 1) << 3), 2 * kp + (mi & 1)), bq[0], bq[1], bq[2],
+                            bq[3]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t a[4];
+                        q_frag(2 * kp + j, a);
+                        MmaOp<__half>::run(s[j][0], a, e4m3x2_to_half2(bq[j]), e4m3x2_hi_to_half2(bq[j]));
+                        MmaOp<__half>::run(s[j][NB - 1], a, e4m3x2_to_half2(bq[2 + j]), e4m3x2_hi_to_half2(bq[2 + j]));
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_empty[kst]);
+        const int box = (it * NT + key0) >> p.box_shift;
+        const float kss = ksc[box], lv = lvs[box], inv = exp2f(-lv);
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = kt + key0 + n * 8 + tq * 2 + (e & 1);
+                float& x = s[0][n][e];
+                x += s[1][n][e];
+                if (e < 2) {
+                    x = q8_score(x, c0 * kss, lv, key >= lo0 && key <= hi0, ab0, dg0, key);
+                    mx0 = fmaxf(mx0, x);
+                } else {
+                    x = q8_score(x, c1 * kss, lv, key >= lo1 && key <= hi1, ab1, dg1, key);
+                    mx1 = fmaxf(mx1, x);
+                }
+            }
+        uint8_t* ps = smem + C::OFF_P + (it & 1) * (M * 128);
+        float sum0, sum1;
+        auto weights = [&]() {
+            const float ma = mine(0), mb = mine(1);
+            const float u0 = ma == -INFINITY ? 0.f : ma - kQ8Offset, u1 = mb == -INFINITY ? 0.f : mb - kQ8Offset;
+            sum0 = sum1 = 0.f;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const float w0 = fast_exp2(s[0][n][0] - u0), w1 = fast_exp2(s[0][n][1] - u0);
+                const float w2 = fast_exp2(s[0][n][2] - u1), w3 = fast_exp2(s[0][n][3] - u1);
+                sum0 += w0 + w1;
+                sum1 += w2 + w3;
+                const int col = key0 + n * 8;  // a 16-byte unit of eight keys
+                *reinterpret_cast<uint32_t*>(ps + swz128(r0, col >> 3) + tq * 4) = pack2<__half>(w0, w1);
+                *reinterpret_cast<uint32_t*>(ps + swz128(r1, col >> 3) + tq * 4) = pack2<__half>(w2, w3);
+            }
+        };
+        weights();
+        const bool grow = mx0 > mine(0) + 5.f || mx1 > mine(1) + 5.f;
+        if (named_barrier_or(1, NW * 32, grow || !ok)) {  // also publishes the weights
+            if (named_barrier_or(2, NW * 32, !ok)) {
+                ok = false;
+                break;
+            }
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+            if (tq == 0) {
+                xmax[slice * M + r0] = mx0;
+                xmax[slice * M + r1] = mx1;
+            }
+            named_barrier_sync(1, NW * 32);
+#pragma unroll
+            for (int g = 0; g < MG; ++g) {
+                float f[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float nm = m[g][q];
+#pragma unroll
+                    for (int k = 0; k < C::KS; ++k) nm = fmaxf(nm, xmax[k * M + g * 16 + gq + 8 * q]);
+                    f[q] = nm == -INFINITY ? 1.f : fast_exp2(m[g][q] - nm);
+                    m[g][q] = nm;
+                }
+#pragma unroll
+                for (int n = 0; n < 8; ++n) {
+                    o[g][n][0] *= f[0];
+                    o[g][n][1] *= f[0];
+                    o[g][n][2] *= f[1];
+                    o[g][n][3] *= f[1];
+                }
+                if (g == rg) {
+                    l0 *= f[0];
+                    l1 *= f[1];
+                }
+            }
+            weights();
+            named_barrier_sync(1, NW * 32);
+        }
+        l0 = fmaf(sum0, inv, l0);
+        l1 = fmaf(sum1, inv, l1);
+        if (ok) ok = __all_sync(0xffffffffu, q8_wait(&v_full[vst], (it / C::VST) & 1, abort_flag, p.err, p.wait_ns));
+        // V rows that no row attends -> 0, each warp the columns it reads
+        const int z_lo = max(tv.lo - kt, 0), z_hi = min(tv.hi + 1 - kt, NT);
+        const bool zeroed = z_lo > 0 || z_hi < NT;
+        if (zeroed) {
+            uint8_t* vp = smem + C::OFF_V + vst * C::TILE;
+            for (int idx = lane; idx < NT * 4; idx += 32) {
+                const int r = idx >> 2;
+                if (r < z_lo || r >= z_hi)
+                    *reinterpret_cast<uint4*>(vp + q8_off<DP, NT>(r, warp * 4 + (idx & 3))) = make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+        }
+        if (ok) {
+            const uint32_t p_base = smem_addr(ps);
+#pragma unroll
+            for (int ks = 0; ks < NT / 16; ++ks) {
+                uint32_t a[MG][4];
+#pragma unroll
+                for (int g = 0; g < MG; ++g)
+                    ldsm_x4(p_base + swz128(g * 16 + rr + ((mi & 1) << 3), 2 * ks + (mi >> 1)), a[g][0], a[g][1], a[g][2],
+                            a[g][3]);
+#pragma unroll
+                for (int np = 0; np < 2; ++np) {
+                    uint32_t v[4];
+                    ldsm_x4_t(v_base + q8_off<DP, NT>(ks * 16 + rr + ((mi & 1) << 3), warp * 4 + 2 * np + (mi >> 1)), v[0],
+                              v[1], v[2], v[3]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = __byte_perm(v[e], 0, 0x3120);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t e0 = e4m3x2_to_half2(v[2 * j]), e1 = e4m3x2_to_half2(v[2 * j + 1]);
+                        const uint32_t d0 = e4m3x2_hi_to_half2(v[2 * j]), d1 = e4m3x2_hi_to_half2(v[2 * j + 1]);
+#pragma unroll
+                        for (int g = 0; g < MG; ++g) {
+                            MmaOp<__half>::run(o[g][2 * (2 * np + j)], a[g], e0, e1);
+                            MmaOp<__half>::run(o[g][2 * (2 * np + j) + 1], a[g], d0, d1);
+                        }
+                    }
+                }
+            }
+        }
+        if (zeroed) fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_empty[vst]);
+    }
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+    l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+    if (named_barrier_or(1, NW * 32, !ok || *abort_flag != 0u)) return;
+    if (tq == 0) {
+        xmax[slice * M + r0] = l0;
+        xmax[slice * M + r1] = l1;
+    }
+    named_barrier_sync(1, NW * 32);
+    T* out = static_cast<T*>(p.out);
+#pragma unroll
+    for (int g = 0; g < MG; ++g)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int row = g * 16 + gq + 8 * q;
+            if (row >= tv.rows) continue;
+            float L = 0.f;
+#pragma unroll
+            for (int k = 0; k < C::KS; ++k) L += xmax[k * M + row];
+            const float iv = L == 0.f ? 0.f : 1.f / L;
+            const int rho = tv.row0 + row;
+            const int i = rho / p.G, gg = rho - i * p.G;
+            const int64_t t = tv.q0 + i;
+            const int h = hk * p.G + gg;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int d = warp * 64 + u * 16 + tq * 4;
+                if (d >= p.D) continue;
+                const float x0 = o[g][2 * u][2 * q] * iv, x1 = o[g][2 * u + 1][2 * q] * iv;
+                const float x2 = o[g][2 * u][2 * q + 1] * iv, x3 = o[g][2 * u + 1][2 * q + 1] * iv;
+                if (single)
+                    *reinterpret_cast<uint2*>(out + t * p.o_s0 + (int64_t)h * p.o_s1 + d) =
+                        make_uint2(pack2<T>(x0, x1), pack2<T>(x2, x3));
+                else
+                    *reinterpret_cast<float4*>(p.part_o + ((int64_t)split * p.part_stride + t * p.H + h) * p.D + d) =
+                        make_float4(x0, x1, x2, x3);
+            }
+            if (warp == 0 && tq == 0) {
+                const float lse = L == 0.f ? -INFINITY : (m[g][q] - kQ8Offset + log2f(L)) * 0.69314718055994531f;
+                if (single)
+                    p.lse[(int64_t)h * p.lse_s0 + t + (int64_t)b * p.lse_sb] = lse;
+                else
+                    p.part_lse[(int64_t)split * p.part_stride + t * p.H + h] = lse;
+            }
+        }
+}
+
+}  // namespace pa

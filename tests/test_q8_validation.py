@@ -108,6 +108,53 @@ def test_q8_append_head_major_scales():
     assert q8(ks=desc([6, 2], F32, [1, 6]), vs=desc([6, 2], F32, [1, 6])) == 0
 
 
+def attend(**over):
+    d = dict(q=desc([8, 4, 64], BF), k=desc([6, 32, 2, 64], E4), v=desc([6, 32, 2, 64], E4), ks=desc([6, 2], F32),
+             vs=desc([6, 2], F32), cu_q=desc([3], I32), cu_k=desc([3], I32), bt=desc([2, 3], I32), alibi=None,
+             out=desc([8, 4, 64], BF), lse=desc([4, 8], F32))
+    P, sk, D, H, scale = (over.pop(k, v) for k, v in (("P", 32), ("sk", 96), ("D", 64), ("H", 4), ("scale", 0.125)))
+    d.update(over)
+    return binding.varlen_check_q8(list(d.values()), 5, sk, H, 2, D, P, scale)
+
+
+def test_q8_attention_well_formed():
+    assert attend() == 0
+    assert attend(alibi=desc([4], F32)) == 0
+    assert attend(ks=desc([6, 2], F32, [1, 6])) == 0
+
+
+@pytest.mark.parametrize("name,over", [
+    ("PA_ERR_ARG", dict(bt=None)),  # always paged
+    ("PA_ERR_ARG", dict(q=None)),
+    ("PA_ERR_ARG", dict(vs=None)),
+    ("PA_ERR_RANK", dict(q=desc([8, 256], BF))),
+    ("PA_ERR_RANK_PAGED", dict(k=desc([192, 2, 64], E4))),
+    ("PA_ERR_NONCONTIG", dict(k=desc([6, 32, 2, 64], E4, [8192, 256, 128, 2]))),
+    ("PA_ERR_SHAPE", dict(v=desc([7, 32, 2, 64], E4))),
+    ("PA_ERR_PAGE_UNSET", dict(P=0)),
+    ("PA_ERR_PAGE_MISMATCH", dict(P=64)),
+    ("PA_ERR_PAGE_MULT32", dict(k=desc([6, 48, 2, 64], E4), v=desc([6, 48, 2, 64], E4), P=48)),
+    ("PA_ERR_SHAPE", dict(alibi=desc([5], F32))),
+    ("PA_ERR_UNSUPPORTED", dict(q=desc([8, 4, 64], F32))),
+    ("PA_ERR_ARG", dict(k=desc([6, 32, 2, 64], BF))),
+    ("PA_ERR_ARG", dict(v=desc([6, 32, 2, 64], BF))),
+    ("PA_ERR_ARG", dict(out=desc([8, 4, 64], binding.PA_F16))),
+    ("PA_ERR_RANK", dict(ks=desc([12], F32))),
+    ("PA_ERR_SHAPE", dict(vs=desc([6, 3], F32))),
+    ("PA_ERR_ARG", dict(vs=desc([6, 2], BF))),
+    ("PA_ERR_ARG", dict(sk=97)),  # the table is too narrow
+    ("PA_ERR_ARG", dict(H=8)),
+    ("PA_ERR_ARG", dict(scale=float("nan"))),
+    ("PA_ERR_UNSUPPORTED", dict(k=desc([6, 32, 2, 64], E4, [4104, 128, 64, 1]), v=desc([6, 32, 2, 64], E4, [4104, 128, 64, 1]))),
+    ("PA_ERR_UNSUPPORTED", dict(q=desc([8, 4, 72], BF), out=desc([8, 4, 72], BF), k=desc([6, 32, 2, 72], E4),
+                                v=desc([6, 32, 2, 72], E4), D=72)),
+    ("PA_ERR_UNSUPPORTED", dict(k=desc([6, 32, 2, 64], E4, None, 0x100008))),
+])
+def test_q8_attention_refusals(name, over):
+    assert binding.STATUS[attend(**over)] == name
+    assert binding.last_error()
+
+
 # ---- the plain implementations themselves ----
 
 def test_plain_e4m3_is_torchs():
