@@ -548,7 +548,7 @@ int validate_q8(const pa_tensor* q, const pa_tensor* k, const pa_tensor* v, cons
     // the row tiles of sequences that no tensor-core prefill kernel takes, in grid.y
     const int64_t rows = std::max<int64_t>(1, (int64_t)max_sq * (a->H / a->Hkv));
     const int64_t row_tiles = rows <= 16 ? 1 : (rows + 31) / 32;
-    if ((int64_t)a->Hkv * row_tiles > 65535)
+    if (!pa::prefill_q8_supported(*a) && (int64_t)a->Hkv * row_tiles > 65535)
         return fail(PA_ERR_UNSUPPORTED,
                     "num_heads_k (%d) x row tiles of max_seqlen_q x group (%lld) exceeds 65535 CTAs per sequence; split "
                     "the call into shorter query chunks",
@@ -957,7 +957,8 @@ int launch_forward(pa::Args& a, void* stream, ScratchFn scratch, void* scratch_c
     int ce = pa::error_word(&err);
     if (ce != cudaSuccess) return fail(PA_ERR_CUDA, "error word: %s", cudaGetErrorString((cudaError_t)ce));
 
-    const bool use_prefill = a.k_scale ? false : pa::prefill_supported(a);
+    const bool use_prefill = a.k_scale ? pa::prefill_q8_supported(a) : pa::prefill_supported(a);
+    const auto launch_prefill = a.k_scale ? pa::launch_prefill_q8 : pa::launch_prefill;
     // SMs the persistent prefill grid may hold beside the decode-class pass (it runs before
     // that pass, not beside it, when there is no side stream)
     const int prefill_sms =
@@ -977,7 +978,7 @@ int launch_forward(pa::Args& a, void* stream, ScratchFn scratch, void* scratch_c
     }
     int* counter = use_prefill ? reinterpret_cast<int*>(static_cast<char*>(ws) + counter_at) : nullptr;
     if (!use_prefill || !side_stream_ok) {
-        if (use_prefill && (rc = pa::launch_prefill(a, counter, err, g_msg, sizeof g_msg)) != PA_OK) return rc;
+        if (use_prefill && (rc = launch_prefill(a, counter, err, g_msg, sizeof g_msg)) != PA_OK) return rc;
         rc = pa::launch_splitkv(a, plan, ws, err, g_msg, sizeof g_msg);
         if (rc != PA_OK) return rc;
         g_msg[0] = '\0';
@@ -992,7 +993,7 @@ int launch_forward(pa::Args& a, void* stream, ScratchFn scratch, void* scratch_c
     if (e != cudaSuccess) return fail(PA_ERR_CUDA, "forking the prefill stream: %s", cudaGetErrorString(e));
     pa::Args ap = a;
     ap.stream = ss->stream;
-    rc = pa::launch_prefill(ap, counter, err, g_msg, sizeof g_msg);
+    rc = launch_prefill(ap, counter, err, g_msg, sizeof g_msg);
     if (rc == PA_OK) rc = pa::launch_splitkv(a, plan, ws, err, g_msg, sizeof g_msg);
     // join even after a failed launch, so the caller's stream never runs ahead of the side stream
     e = cudaEventRecord(ss->join, ss->stream);

@@ -97,6 +97,9 @@ int prefill_rows_threshold();  // sequences with sq*G > this go to the prefill k
 // zeroes on a.stream before the kernel.
 constexpr size_t kPrefillCounterBytes = 256;
 int launch_prefill(const Args& a, int* counter, unsigned int* err, char* msg, size_t msg_len);
+// The same over an 8-bit cache (prefill_q8.cu).
+bool prefill_q8_supported(const Args& a);
+int launch_prefill_q8(const Args& a, int* counter, unsigned int* err, char* msg, size_t msg_len);
 // Upper bound of the prefill kernel's work items (its grid is min(SMs, items)).
 int64_t prefill_items_bound(const Args& a);
 

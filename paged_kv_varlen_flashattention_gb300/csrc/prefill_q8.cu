@@ -1,0 +1,890 @@
+// Tensor-core prefill / chunked prefill over an 8-bit paged cache (sm_103a), head_dim <= 128.
+//
+// The structure of prefill_kernel (prefill_tc.cu): one persistent CTA per SM takes items of two
+// 128-row query tiles (A, B) of one (sequence, kv head) from a device counter, so every K/V
+// tile feeds both; S, P and O live in tensor memory.  What the 8-bit cache changes:
+//
+//  * Q.K^T runs on the 8-bit tensor cores with K as it is in the cache (no conversion, half the
+//    shared memory).  q is written as a sum of e4m3 terms, q 2^e = t0 + t1 [+ t2], each the
+//    rounding of what the ones before leave, and the terms' products accumulate in the same S.
+//    A term takes 4 significant bits and its remainder is at most half its last place, so two
+//    terms hold bf16's 8 bits and three hold f16's 11; e, a power of two per row, brings the row's
+//    largest magnitude to 224..448, so what a term cannot hold (half of e4m3's smallest step, 2^-10)
+//    is at most 2^-17.8 of that largest.  An 8-bit product takes half the time of a 16-bit one, so two terms cost what
+//    one bf16 product does.
+//  * P.V runs on f16: converter warps read the V tiles as TMA leaves them, turn the codes into
+//    f16 (exact) in the layout the matrix unit reads, and zero the rows of keys that no row of
+//    the item attends (0 x NaN is NaN).  P is f16 too, in every call.
+//  * A page's scales enter the softmax as in q8_decode.cuh: x = c ks s + log2 vs, weights
+//    2^(x - m + 7), l = sum of weights / vs, per group of 32 keys (pages are multiples of 32).
+//    The reference m is raised only when some x is more than 8 above it, so weights are at most
+//    2^15, within f16.
+//
+// Roles (512 threads, four warpgroups):
+//   warp 0       takes items and publishes them; K tiles and their scales
+//   warp 2       V tiles
+//   warps 1, 3   MMA issuers of tiles A and B
+//   warps 4..11  softmax, 16 rows (TMEM lanes) of each tile a warp, four threads a row
+//   warps 12..15 converters: q into its terms at the start of an item, then V tile by tile
+//
+// Tensor-core bound: 4 D flops per (row, key) at the f16 rate (f16 q: 5 D).
+#include <algorithm>
+#include <cfloat>
+#include <cstdio>
+#include <cstdlib>
+#include <type_traits>
+
+#include "prefill_common.cuh"
+#include "q8_common.cuh"
+#include "rope_common.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kPqThreads = 512;
+// Register split (setmaxnreg) of the launch's 512 x 128: control 56, softmax 192, converters 72:
+// 128 x 56 + 256 x 192 + 128 x 72 = 65,536.
+constexpr int kPqRegsControl = 56, kPqRegsSoftmax = 192, kPqRegsConvert = 72;
+constexpr float kPqOffset = 7.f;
+
+struct PrefillQ8Params : PrefillParams {
+    const void* q;
+    int64_t q_s0, q_s1;
+    const float* ks;
+    const float* vs;
+    int64_t ks_s0, ks_s1, vs_s0, vs_s1;
+};
+
+// DP: padded head dim, 64 or 128 (rows of the 8-bit tiles are 128 bytes either way, zero filled
+// past the head dim); NTERM: e4m3 terms of q.
+template <int DP, int NTERM>
+struct PqCfg {
+    static constexpr int TILE = 128 * 128;  // a q term, a K tile, a V tile as loaded
+    static constexpr int KS = NTERM == 2 ? 3 : 2, VR = 2;
+    static constexpr int VC_TILE = (DP / 64) * TILE;  // a V tile in f16
+    static constexpr int OFF_Q = 0;                   // tile x, term t at (x NTERM + t) TILE
+    static constexpr int OFF_K = 2 * NTERM * TILE;
+    static constexpr int OFF_VR = OFF_K + KS * TILE;
+    static constexpr int OFF_VC = OFF_VR + VR * TILE;
+    static constexpr int OFF_BAR = OFF_VC + 2 * VC_TILE;
+    // q_full, k_full[KS], k_empty[KS], vr_full[VR], vr_empty[VR], vc_full[2], vc_empty[2], s_full[2],
+    // p_full[2], pv_done[2], drain[2], item_ready[2], item_free[2], q_free
+    static constexpr int NBAR = 2 + 2 * KS + 2 * VR + 16;
+    static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem base, abort flag
+    static constexpr int OFF_SLOT = OFF_MISC + 16;       // two item slots
+    static constexpr int SC_RING = 8;
+    static constexpr int OFF_SC = OFF_SLOT + 128;        // [K ring position % 8]: ks[4], log2 vs[4], 1 / vs[4]
+    static constexpr int OFF_EXP = OFF_SC + SC_RING * 48;  // [item parity][tile][row]: e of the row, int8
+    static constexpr int SMEM = OFF_EXP + 512 + 1024;
+    static constexpr uint32_t T_S0 = 0, T_S1 = 128, T_O0 = 256, T_O1 = 256 + DP;
+    // The scale ring: the K producer writes position g after stage g % KS was released, when every
+    // softmax warp is at tile g - KS - 1 or later, so what it overwrites (g - 8) has been read.
+    static_assert(KS + 1 < SC_RING, "scale ring");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+};
+
+template <typename T, int DP, bool ALIBI>
+__global__ void __launch_bounds__(kPqThreads, 1)
+    prefill_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const PrefillQ8Params p) {
+    constexpr int NTERM = std::is_same<T, __half>::value ? 3 : 2;
+    using C = PqCfg<DP, NTERM>;
+    constexpr int KS = C::KS, VR = C::VR;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* q_free = q_full + 1;
+    uint64_t* k_full = q_free + 1;
+    uint64_t* k_empty = k_full + KS;
+    uint64_t* vr_full = k_empty + KS;
+    uint64_t* vr_empty = vr_full + VR;
+    uint64_t* vc_full = vr_empty + VR;
+    uint64_t* vc_empty = vc_full + 2;
+    uint64_t* s_full = vc_empty + 2;       // [tile]
+    uint64_t* p_full = s_full + 2;         // [tile]
+    uint64_t* pv_done = p_full + 2;        // [tile]
+    uint64_t* drain = pv_done + 2;         // [issuer]
+    uint64_t* item_ready = drain + 2;      // [slot]
+    uint64_t* item_free = item_ready + 2;  // [slot]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+    PfItem* slots = reinterpret_cast<PfItem*>(smem + C::OFF_SLOT);
+    float* sc_ring = reinterpret_cast<float*>(smem + C::OFF_SC);
+    int8_t* row_exp = reinterpret_cast<int8_t*>(smem + C::OFF_EXP);
+    if (tid == 64) {
+        mbar_init(q_full, 4);  // converter warps
+        mbar_init(q_free, 2);
+        for (int s = 0; s < KS; ++s) {
+            mbar_init(&k_full[s], 2);   // the copies, the scales
+            mbar_init(&k_empty[s], 2);  // one arrive per query tile: the softmax, or issuer B without a tile B
+        }
+        for (int s = 0; s < VR; ++s) {
+            mbar_init(&vr_full[s], 1);
+            mbar_init(&vr_empty[s], 4);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&vc_full[x], 4);
+            mbar_init(&vc_empty[x], 2);
+            mbar_init(&s_full[x], 1);
+            mbar_init(&p_full[x], 8);
+            mbar_init(&pv_done[x], 1);
+            mbar_init(&drain[x], 1);
+            mbar_init(&item_ready[x], 1);
+            mbar_init(&item_free[x], 15);  // the V producer, two issuers, eight softmax warps, four converters
+        }
+        *abort_flag = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(tmem_slot, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = *tmem_slot;
+    const int qpt = 128 / p.G;    // whole queries per 128-row tile
+    const int trows = qpt * p.G;  // rows of a tile that hold queries
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) {
+        const bool r = __all_sync(0xffffffffu, wait_bar(bar, parity, abort_flag, p.err, p.wait_ns));
+        tc::fence_after_sync();
+        return r;
+    };
+    auto take_slot = [&](int k, PfItem& it) -> bool {
+        if (!wait_all(&item_ready[k & 1], (k >> 1) & 1)) return false;
+        it = slots[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&item_free[k & 1]);
+        return true;
+    };
+    // The item's key tiles into the K ring (with the scales of each tile's four 32-key groups) or the V
+    // ring.  Lane i holds the block id (and scales) of box i of a window of 32 boxes.
+    auto produce = [&](const PfItem& it, const CUtensorMap* map, uint8_t* ring, uint64_t* fullb, uint64_t* emptyb,
+                       int stages, int g0, bool scales) -> bool {
+        const int32_t* bt_row = p.bt + (int64_t)it.b * p.bt_s0;
+        const int bpt = p.boxes_per_tile, win_tiles = 32 / bpt;
+        int jw = -win_tiles, id = -1;
+        float ksc = 0.f, vsc = 0.f;
+        for (int j = 0; j < it.n_tiles; ++j) {
+            if (j >= jw + win_tiles) {
+                jw = j;
+                const int key = it.kt0 + j * 128 + lane * p.box_rows;
+                id = box_block(bt_row, p.bt_cols, p.num_blocks, p.P, key, it.sk, p.err);
+                if (scales && id >= 0) {
+                    ksc = __ldg(p.ks + (int64_t)id * p.ks_s0 + (int64_t)it.hk * p.ks_s1);
+                    vsc = __ldg(p.vs + (int64_t)id * p.vs_s0 + (int64_t)it.hk * p.vs_s1);
+                }
+            }
+            const int g = g0 + j, s = g % stages;
+            if (g >= stages && !wait_all(&emptyb[s], ((g / stages) - 1) & 1)) return false;
+            int blk[4];
+            uint32_t bytes = 0;
+#pragma unroll
+            for (int jj = 0; jj < 4; ++jj) {
+                const int b = __shfl_sync(0xffffffffu, id, ((j - jw) * bpt + jj) & 31);
+                blk[jj] = jj < bpt ? b : -1;
+                if (blk[jj] >= 0) bytes += (uint32_t)(p.box_rows * 128);
+            }
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&fullb[s], bytes);
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj) {
+                    if (blk[jj] < 0) continue;
+                    const int key = it.kt0 + j * 128 + jj * p.box_rows;
+                    tma_load_4d(ring + s * C::TILE + jj * p.box_rows * 128, map, &fullb[s], 0, it.hk,
+                                key - (key / p.P) * p.P, blk[jj], 0ull);
+                }
+            }
+            __syncwarp();
+            if (scales) {  // after the copies are on their way: the gather's latency runs beside theirs
+                const int src = (j - jw) * bpt + ((lane & 3) * 32) / p.box_rows;
+                const float a = __shfl_sync(0xffffffffu, ksc, src), v = __shfl_sync(0xffffffffu, vsc, src);
+                if (lane < 4) {
+                    float* slot = sc_ring + (g % C::SC_RING) * 12 + lane;
+                    const float lv = v > 7.8886090522101181e-31f ? fminf(log2f(v), 126.f) : (float)kScaleExpMin;
+                    slot[0] = a;
+                    slot[4] = lv;
+                    slot[8] = exp2f(-lv);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&fullb[s]);
+            }
+        }
+        return true;
+    };
+
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPqRegsControl));
+    if (warp == 0) {
+        // ---------------- item taker, K producer ----------------
+        // Items as in prefill_kernel: w = pair * Hkv + kv head, each sequence's last pair first.
+        const int total = p.pairs * p.Hkv;
+        if (!p.withhold) prefetch_tmap(&tm_k);
+        int w_next = lane == 0 ? atomicAdd(p.counter, 1) : 0;
+        int gk = 0;
+        for (int k = 0;; ++k) {
+            const int w = __shfl_sync(0xffffffffu, w_next, 0);
+            PfItem it{};
+            it.b = -1;
+            if (w < total) {
+                const int pair = w / p.Hkv;
+                it.hk = w - pair * p.Hkv;
+                int remaining = pair;
+                for (int base = 0; base < p.batch && it.b < 0; base += 32) {
+                    const int bb = base + lane;
+                    int pairs = 0;
+                    if (bb < p.batch) {
+                        const int sqb = p.cu_q[bb + 1] - p.cu_q[bb];
+                        pairs = (int64_t)sqb * p.G > p.rows_cap ? (sqb + 2 * qpt - 1) / (2 * qpt) : 0;
+                    }
+                    int incl = pairs;
+#pragma unroll
+                    for (int off = 1; off < 32; off <<= 1) {
+                        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+                        if (lane >= off) incl += v;
+                    }
+                    const unsigned hit = __ballot_sync(0xffffffffu, remaining < incl);
+                    if (hit) {
+                        const int src = __ffs(hit) - 1;
+                        const int excl = __shfl_sync(0xffffffffu, incl - pairs, src);
+                        const int cnt = __shfl_sync(0xffffffffu, pairs, src);
+                        it.b = base + src;
+                        it.u = cnt - 1 - (remaining - excl);
+                    } else {
+                        remaining -= __shfl_sync(0xffffffffu, incl, 31);
+                    }
+                }
+                if (it.b >= 0) pf_item(p, qpt, it);
+            }
+            if (it.b >= 0 && lane == 0) w_next = atomicAdd(p.counter, 1);
+            if (k >= 2 && !wait_all(&item_free[k & 1], ((k >> 1) - 1) & 1)) break;
+            if (lane == 0) {
+                slots[k & 1] = it;
+                mbar_arrive(&item_ready[k & 1]);
+            }
+            if (it.b < 0) break;
+            if (it.bad) {
+                if (lane == 0) flag_error(p.err, PA_ERR_DEVICE_BOUNDS);
+                continue;
+            }
+            if (it.n_tiles == 0) continue;
+            if (!p.withhold && !produce(it, &tm_k, smem + C::OFF_K, k_full, k_empty, KS, gk, true)) break;
+            gk += it.n_tiles;
+        }
+    } else if (warp == 2) {
+        // ---------------- V producer ----------------
+        if (!p.withhold) prefetch_tmap(&tm_v);
+        int gv = 0;
+        for (int k = 0;; ++k) {
+            PfItem it;
+            if (!take_slot(k, it) || it.b < 0) break;
+            if (it.bad || it.n_tiles == 0) continue;
+            if (!p.withhold && !produce(it, &tm_v, smem + C::OFF_VR, vr_full, vr_empty, VR, gv, false)) break;
+            gv += it.n_tiles;
+        }
+    } else {
+        // ---------------- MMA issuers: warp 1 for tile A, warp 3 for tile B ----------------
+        constexpr uint32_t IDESC_S = tc::idesc_e4m3(128, 128);
+        constexpr uint32_t IDESC_O = tc::idesc_f16(128, DP, false, false, true);
+        const int x = warp == 1 ? 0 : 1;
+        const uint64_t da = tc::smem_desc_sw128(smem_addr(smem + C::OFF_Q + x * NTERM * C::TILE), 16, 1024);
+        const uint64_t dk0 = tc::smem_desc_sw128(smem_addr(smem + C::OFF_K), 16, 1024);
+        const uint64_t dv0 = tc::smem_desc_sw128(smem_addr(smem + C::OFF_VC), C::TILE, 1024);
+        const uint32_t d_s = tmem + (x ? C::T_S1 : C::T_S0);
+        const uint32_t d_o = tmem + (x ? C::T_O1 : C::T_O0);
+        int lq = 0, gk = 0, gv = 0, sx = 0;
+        bool ok = true;
+        auto issue_s = [&](int g) {  // S_x = (sum of q terms) K^T of the K tile at ring position g
+            const uint64_t db = dk0 + (uint64_t)((g % KS) * (C::TILE >> 4));
+#pragma unroll
+            for (int t = 0; t < NTERM; ++t)
+#pragma unroll
+                for (int kk = 0; kk < DP / 32; ++kk)
+                    tc::mma_f8_ss_elect(d_s, da + (uint64_t)(t * (C::TILE >> 4) + kk * 2), db + (uint64_t)(kk * 2), IDESC_S,
+                                        t + kk > 0 ? 1u : 0u);
+            tc::commit_elect(&s_full[x]);
+        };
+        for (int k = 0; ok; ++k) {
+            PfItem it;
+            if (!take_slot(k, it) || it.b < 0) break;
+            if (it.bad || it.n_tiles == 0) continue;
+            const int n = it.n_tiles;
+            if (!(ok = wait_all(q_full, lq & 1))) break;
+            if (x == 0 || it.has_b) {
+                if (!(ok = wait_all(&k_full[gk % KS], (gk / KS) & 1))) break;
+                issue_s(gk);
+                if (n == 1) tc::commit_elect(q_free);
+                __syncwarp();
+                for (int j = 0; ok && j < n; ++j) {
+                    const int g_v = gv + j;
+                    if (!(ok = wait_all(&vc_full[g_v & 1], (g_v >> 1) & 1))) break;
+                    const bool more = j + 1 < n;
+                    const int g_k = gk + j + 1;
+                    if (more && !(ok = wait_all(&k_full[g_k % KS], (g_k / KS) & 1))) break;
+                    if (!(ok = wait_all(&p_full[x], (sx + j) & 1))) break;
+                    const uint64_t db = dv0 + (uint64_t)((g_v & 1) * (C::VC_TILE >> 4));
+                    const uint32_t first = j > 0 ? 1u : 0u;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        tc::mma_ts_elect(d_o, d_s + kk * 8, db + (uint64_t)(kk * (2048 / 16)), IDESC_O, kk > 0 ? 1u : first);
+                    if (j + 1 == n) tc::commit_elect(&pv_done[x]);
+                    if (more) {
+                        issue_s(g_k);
+                        if (j + 2 == n) tc::commit_elect(q_free);
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                sx += n;
+            } else {
+                // An item without tile B: this issuer goes through the same phases and releases its
+                // share of q and of every stage.  Were it to skip them, its next wait could meet
+                // a barrier whose phase before that one has yet to complete, and pass at once.
+                if (lane == 0) mbar_arrive(q_free);
+                for (int j = 0; ok && j < n; ++j) {
+                    if (!(ok = wait_all(&k_full[(gk + j) % KS], ((gk + j) / KS) & 1))) break;
+                    if (lane == 0) mbar_arrive(&k_empty[(gk + j) % KS]);
+                    if (!(ok = wait_all(&vc_full[(gv + j) & 1], ((gv + j) >> 1) & 1))) break;
+                    if (lane == 0) mbar_arrive(&vc_empty[(gv + j) & 1]);
+                }
+                if (!ok) break;
+            }
+            __syncwarp();
+            gk += n;
+            gv += n;
+            ++lq;
+        }
+        if (lane == 0) {
+            tc::commit(&drain[x]);
+            mbar_wait(&drain[x], 0, p.wait_ns);  // not cut short by an abort: MMAs may be in flight
+        }
+        __syncwarp();
+    }
+    } else if (warp >= 12) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPqRegsConvert));
+    {
+        // ---------------- converters ----------------
+        const int cw = warp - 12;
+        const T* q = static_cast<const T*>(p.q);
+        int ld = 0, gv = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            PfItem it;
+            if (!take_slot(k, it) || it.b < 0) break;
+            if (it.bad || it.n_tiles == 0) continue;
+            // q, once the previous item's last Q.K^T products have completed: half a warp a row, eight
+            // columns a lane; rows without a query keep what is there (their scores are masked)
+            if (ld >= 1 && !(ok = wait_all(q_free, (ld - 1) & 1))) break;
+            const int half = lane >> 4, u = lane & 15;
+            const int passes = it.has_b ? 32 : 16;
+            for (int p0 = 0; p0 < passes; p0 += 4) {
+                uint4 w[4];
+                bool live[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = (p0 + i) * 8 + cw * 2 + half, rr = r & 127;
+                    const int ql = rr / p.G, qi = it.i0 + (r >> 7) * qpt + ql;
+                    live[i] = rr < trows && qi < it.sq;
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (live[i] && u * 8 < p.D)
+                        w[i] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)(it.q0 + qi) * p.q_s0 +
+                                                                    (int64_t)(it.hk * p.G + rr - ql * p.G) * p.q_s1 + u * 8));
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = (p0 + i) * 8 + cw * 2 + half, rr = r & 127;
+                    float y[8];
+                    const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    float mx = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unpack2<T>(ww[e]);
+                        y[2 * e] = f.x;
+                        y[2 * e + 1] = f.y;
+                        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+#pragma unroll
+                    for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    // the largest power of two with mx 2^e2 <= 448 = 1.75 x 2^8
+                    const int bits = __float_as_int(mx);
+                    const int e2 = min(126, 8 - ((bits >> 23) - 127) - ((bits & 0x7fffff) > 0x600000 ? 1 : 0));
+                    const float up = __int_as_float((127 + e2) << 23);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        y[e] *= up;
+                        if (!(fabsf(y[e]) <= FLT_MAX)) y[e] = NAN;  // the row's scores become NaN
+                    }
+                    uint8_t* dst = smem + C::OFF_Q + (r >> 7) * (NTERM * C::TILE) + rr * 128 + (((u >> 1) ^ (rr & 7)) << 4) +
+                                   (u & 1) * 8;
+#pragma unroll
+                    for (int t = 0; t < NTERM; ++t) {
+                        uint32_t c2[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            c2[e] = e4m3x2(y[2 * e], y[2 * e + 1]);
+                            if (t + 1 < NTERM) {
+                                const float2 f = unpack2<__half>(e4m3x2_to_half2(c2[e]));
+                                y[2 * e] -= f.x;
+                                y[2 * e + 1] -= f.y;
+                            }
+                        }
+                        if (live[i])
+                            *reinterpret_cast<uint2*>(dst + t * C::TILE) = make_uint2(c2[0] | (c2[1] << 16), c2[2] | (c2[3] << 16));
+                    }
+                    if (u == 0) row_exp[(ld & 1) * 256 + r] = (int8_t)e2;
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            // V tiles: warp cw converts rows 32 cw .. + 31
+            const int64_t cdiag = (int64_t)it.sk - it.sq;
+            const int i_last = min(it.sq - 1, it.i0 + (it.has_b ? 2 : 1) * qpt - 1);
+            const int key_lo = p.wl >= 0 ? (int)max64(0, it.i0 + cdiag - p.wl) : 0;
+            const int key_hi = p.wr >= 0 ? (int)min64((int64_t)it.sk - 1, i_last + cdiag + p.wr) : it.sk - 1;
+            for (int j = 0; j < it.n_tiles; ++j) {
+                const int g = gv + j, s = g % VR, c = g & 1;
+                if (!(ok = wait_all(&vr_full[s], (g / VR) & 1))) break;
+                if (g >= 2 && !(ok = wait_all(&vc_empty[c], ((g >> 1) - 1) & 1))) break;
+                const uint8_t* src = smem + C::OFF_VR + s * C::TILE;
+                uint8_t* dst = smem + C::OFF_VC + c * C::VC_TILE;
+                const int kt = it.kt0 + j * 128;
+                constexpr int UPR = DP / 16;          // 16-byte units of a row
+                constexpr int RPP = 32 / UPR;         // rows a warp converts a pass
+                const int uu = lane % UPR;
+#pragma unroll 4
+                for (int i = 0; i < 32 / RPP; ++i) {
+                    const int r = cw * 32 + i * RPP + lane / UPR;
+                    uint4 v = *reinterpret_cast<const uint4*>(src + swz128(r, uu));
+                    if (kt + r < key_lo || kt + r > key_hi) v = make_uint4(0, 0, 0, 0);
+                    uint4 a, b;
+                    a.x = e4m3x2_to_half2(v.x);
+                    a.y = e4m3x2_hi_to_half2(v.x);
+                    a.z = e4m3x2_to_half2(v.y);
+                    a.w = e4m3x2_hi_to_half2(v.y);
+                    b.x = e4m3x2_to_half2(v.z);
+                    b.y = e4m3x2_hi_to_half2(v.z);
+                    b.z = e4m3x2_to_half2(v.w);
+                    b.w = e4m3x2_hi_to_half2(v.w);
+                    // two 16-byte units of 64-column chunk uu / 4; the lanes of the second chunk, whose
+                    // rows share the first's banks, write theirs in the other order
+                    uint8_t* d = dst + (uu >> 2) * C::TILE;
+                    const int u0 = (uu & 3) * 2;
+                    const bool sw = (uu & 4) != 0;
+                    *reinterpret_cast<uint4*>(d + swz128(r, u0 + (sw ? 1 : 0))) = sw ? b : a;
+                    *reinterpret_cast<uint4*>(d + swz128(r, u0 + (sw ? 0 : 1))) = sw ? a : b;
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&vc_full[c]);
+                    mbar_arrive(&vr_empty[s]);
+                }
+            }
+            if (!ok) break;
+            gv += it.n_tiles;
+            ++ld;
+        }
+    }
+    } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPqRegsSoftmax));
+    {
+        // ---------------- softmax: tile A and then tile B at every key tile ----------------
+        // Warp w takes TMEM lanes lb .. lb + 15, thread t rows lb + t/4 (q = 0) and + 8 (q = 1), keys
+        // 8 k + 2 (t % 4) + {0, 1}; k / 4 is the 32-key group, whose scales are its page's.
+        const int lg = warp & 3, hh = (warp - 4) >> 2;
+        const int gid = lane >> 2, tig = lane & 3;
+        const int lb = lg * 32 + hh * 16;
+        const uint32_t lane_addr = (uint32_t)lb << 16;
+        T* out = static_cast<T*>(p.out);
+        struct TileRows {
+            int lo[2], hi[2];
+            float m[2], l[2], sl[2];
+            int dg[2];
+            float ab[2];
+        };
+        int qi[2], gi[2];
+        bool pad[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int r = lb + gid + 8 * q;
+            qi[q] = r / p.G;
+            gi[q] = r - qi[q] * p.G;
+            pad[q] = r >= trows;
+        }
+        int gk = 0, gv = 0, sa = 0, sb = 0, aa = 0, ab_ = 0, ld = 0;
+        bool ok = true;
+        for (int k = 0; ok; ++k) {
+            PfItem it;
+            if (!take_slot(k, it) || it.b < 0) break;
+            if (it.bad) continue;
+            const int b = it.b, hk = it.hk;
+            const int64_t cdiag = (int64_t)it.sk - it.sq;
+            const int64_t rows_total = (int64_t)it.sq * p.G;
+            if (it.n_tiles == 0) {  // no row attends any key: out = 0, lse = -inf
+                const int x = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+                const int64_t rho = (int64_t)(it.i0 + x * qpt) * p.G + r;
+                if (r < trows && rho < rows_total) {
+                    const int i = (int)(rho / p.G), g = (int)(rho - (int64_t)i * p.G);
+                    const int64_t t = it.q0 + i;
+                    const int h = hk * p.G + g;
+                    for (int d = 0; d < p.D; d += 8)
+                        *reinterpret_cast<int4*>(out + t * p.o_s0 + (int64_t)h * p.o_s1 + d) = make_int4(0, 0, 0, 0);
+                    p.lse[(int64_t)h * p.lse_s0 + t + (int64_t)b * p.lse_sb] = -INFINITY;
+                }
+                continue;
+            }
+            const int n = it.n_tiles;
+            auto qrow = [&](int x, int q) { return it.i0 + x * qpt + qi[q]; };
+            auto live = [&](int x, int q) { return !pad[q] && qrow(x, q) < it.sq; };
+            auto init_rows = [&](int x, TileRows& st) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    st.lo[q] = 0;
+                    st.hi[q] = -1;
+                    st.dg[q] = 0;
+                    st.ab[q] = 0.f;
+                    if (live(x, q)) {
+                        const int64_t diag = qrow(x, q) + cdiag;
+                        st.lo[q] = p.wl >= 0 ? (int)max64(0, diag - p.wl) : 0;
+                        st.hi[q] = p.wr >= 0 ? (int)max64(-1, min64((int64_t)it.sk - 1, diag + p.wr)) : it.sk - 1;
+                        if (ALIBI) {
+                            st.dg[q] = (int)diag;
+                            st.ab[q] = p.alibi[hk * p.G + gi[q]] * kLog2e;
+                        }
+                    }
+                    st.m[q] = -INFINITY;
+                    st.l[q] = 0.f;
+                    st.sl[q] = 0.f;
+                }
+            };
+            TileRows rows_a, rows_b;
+            init_rows(0, rows_a);
+            init_rows(1, rows_b);
+
+            auto step = [&](int x, TileRows& st, int j) -> bool {
+                const int kt = it.kt0 + j * 128;
+                const int sc = (x ? sb : sa) + j;
+                if (!__all_sync(0xffffffffu, wait_bar(&s_full[x], sc & 1, abort_flag, p.err, p.wait_ns))) return false;
+                tc::fence_after_sync();
+                const uint32_t s_addr = tmem + lane_addr + (x ? C::T_S1 : C::T_S0);
+                const uint32_t o_addr = tmem + lane_addr + (x ? C::T_O1 : C::T_O0);
+                float sv[64];
+                tc::ld_16x256b_x8(s_addr, *reinterpret_cast<float(*)[32]>(&sv[0]));
+                tc::ld_16x256b_x8(s_addr + 64, *reinterpret_cast<float(*)[32]>(&sv[32]));
+                if (warp == 4 && lane == 0) {
+                    mbar_arrive(&k_empty[(gk + j) % KS]);
+                    if (j > 0) mbar_arrive(&vc_empty[(gv + j - 1) & 1]);
+                }
+                // scales of the four 32-key groups; c[q][g] > 0 so that -inf x c stays -inf
+                const float* slot = sc_ring + ((gk + j) % C::SC_RING) * 12;
+                float c[2][4], lv[4];
+                if (j == 0) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int e = row_exp[(ld & 1) * 256 + x * 128 + lb + gid + 8 * q];
+                        st.sl[q] = p.scale_log2 * __int_as_float((127 - e) << 23);
+                    }
+                }
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float ksg = slot[g];
+                    lv[g] = slot[4 + g];
+                    c[0][g] = fmaxf(st.sl[0] * ksg, 1e-37f);
+                    c[1][g] = fmaxf(st.sl[1] * ksg, 1e-37f);
+                }
+                tc::wait_ld();
+                if (!(kt >= max(st.lo[0], st.lo[1]) && kt + 127 <= min(st.hi[0], st.hi[1]))) {
+#pragma unroll
+                    for (int kk = 0; kk < 16; ++kk)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = kt + 8 * kk + 2 * tig + e;
+                                float& v = sv[4 * kk + 2 * q + e];
+                                v = (key >= st.lo[q] && key <= st.hi[q]) ? v : -INFINITY;
+                            }
+                }
+                if (ALIBI) {  // the whole x here: c = 1 and log2 vs = 0 below
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float d0 = (float)(st.dg[q] - kt - 2 * tig);
+#pragma unroll
+                        for (int kk = 0; kk < 16; ++kk)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float& v = sv[4 * kk + 2 * q + e];
+                                v = fmaf(-st.ab[q], fabsf(d0 - (float)(8 * kk + e)), fmaf(v, c[q][kk >> 2], lv[kk >> 2]));
+                            }
+                    }
+                }
+                float lm[2];
+                bool grow = false;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    lm[q] = -INFINITY;
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float* v = &sv[16 * g + 2 * q];
+                        float t = fmaxf(v[0], v[1]);
+#pragma unroll
+                        for (int kk = 1; kk < 4; ++kk) t = max3f(t, v[4 * kk], v[4 * kk + 1]);
+                        lm[q] = fmaxf(lm[q], ALIBI ? t : fmaf(t, c[q][g], lv[g]));
+                    }
+                    grow |= lm[q] > st.m[q] + 8.f;
+                }
+                float alpha[2] = {1.f, 1.f};
+                if (__any_sync(0xffffffffu, grow)) {
+                    bool resc = false;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float mx = lm[q];
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        if (mx > st.m[q] + 8.f) {
+                            alpha[q] = fast_exp2(st.m[q] - mx);
+                            st.m[q] = mx;
+                            resc = true;
+                        }
+                    }
+                    // O_x's last P.V (PV_x(j-1)) precedes S_x(j) on its issuer: complete now
+                    if (j > 0 && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+                        for (int cc = 0; cc < DP / 64; ++cc) {
+                            float o[32];
+                            tc::ld_16x256b_x8(o_addr + cc * 64, o);
+                            tc::wait_ld();
+                            uint32_t ob[32];
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e] * alpha[(e >> 1) & 1]);
+                            tc::st_16x256b_x8(o_addr + cc * 64, ob);
+                        }
+                    }
+                }
+                float nm[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    nm[q] = st.m[q] == -INFINITY ? 0.f : kPqOffset - st.m[q];
+                    st.l[q] *= alpha[q];
+                }
+                uint32_t pk[32];
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float inv = slot[8 + g];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const float cg = ALIBI ? 1.f : c[q][g], ag = ALIBI ? nm[q] : nm[q] + lv[g];
+                        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+                        for (int k4 = 0; k4 < 4; ++k4) {
+                            const int kk = 4 * g + k4;
+                            float x0, x1;
+                            ffma2(x0, x1, sv[4 * kk + 2 * q], sv[4 * kk + 2 * q + 1], cg, cg, ag, ag);
+                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                            fadd2_acc(s0, s1, p0, p1);
+                            pk[2 * kk + q] = pack2<__half>(p0, p1);
+                        }
+                        st.l[q] = fmaf(s0 + s1, inv, st.l[q]);
+                    }
+                }
+                tc::st_16x128b_x16(s_addr, pk);
+                tc::wait_st();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[x]);
+                return true;
+            };
+
+            auto epilogue = [&](int x, TileRows& st) -> bool {
+                if (!__all_sync(0xffffffffu,
+                                wait_bar(&pv_done[x], (x ? ab_ : aa) & 1, abort_flag, p.err, p.wait_ns)))
+                    return false;
+                tc::fence_after_sync();
+                if (warp == 4 && lane == 0) mbar_arrive(&vc_empty[(gv + n - 1) & 1]);
+                const uint32_t o_addr = tmem + lane_addr + (x ? C::T_O1 : C::T_O0);
+                float inv[2];
+                T* orow[2];
+                bool valid[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    float l = st.l[q];
+                    l += __shfl_xor_sync(0xffffffffu, l, 1);
+                    l += __shfl_xor_sync(0xffffffffu, l, 2);
+                    inv[q] = l == 0.f ? 0.f : 1.f / l;
+                    valid[q] = live(x, q);
+                    const int64_t t = it.q0 + qrow(x, q);
+                    const int h = hk * p.G + gi[q];
+                    orow[q] = out + t * p.o_s0 + (int64_t)h * p.o_s1;
+                    if (valid[q] && tig == 0)
+                        p.lse[(int64_t)h * p.lse_s0 + t + (int64_t)b * p.lse_sb] =
+                            l == 0.f ? -INFINITY : (st.m[q] - kPqOffset + log2f(l)) * 0.69314718055994531f;
+                }
+                // a 4 x 4 transpose over each quad: two 16-byte stores per row and 64-column chunk
+#pragma unroll 1
+                for (int cc = 0; cc < DP / 64; ++cc) {
+                    float o[32];
+                    tc::ld_16x256b_x8(o_addr + cc * 64, o);
+                    tc::wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            w[kk] = pack2<T>(o[4 * kk + 2 * q] * inv[q], o[4 * kk + 2 * q + 1] * inv[q]);
+                        quad_transpose(*reinterpret_cast<uint32_t(*)[4]>(&w[0]), tig);
+                        quad_transpose(*reinterpret_cast<uint32_t(*)[4]>(&w[4]), tig);
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int d = cc * 64 + 32 * hf + 8 * tig;
+                            if (valid[q] && d < p.D)
+                                *reinterpret_cast<uint4*>(orow[q] + d) =
+                                    make_uint4(w[4 * hf], w[4 * hf + 1], w[4 * hf + 2], w[4 * hf + 3]);
+                        }
+                    }
+                }
+                tc::fence_before_sync();  // before this warp's next arrival on p_full[x]
+                return true;
+            };
+
+            for (int j = 0; ok && j < n; ++j) {
+                ok = step(0, rows_a, j);
+                if (ok && it.has_b) ok = step(1, rows_b, j);
+            }
+            if (ok) ok = epilogue(0, rows_a);
+            if (ok && it.has_b) ok = epilogue(1, rows_b);
+            sa += n;
+            ++aa;
+            if (it.has_b) {
+                sb += n;
+                ++ab_;
+            }
+            gk += n;
+            gv += n;
+            ++ld;
+        }
+        tc::fence_before_sync();
+    }
+    }
+    __syncwarp();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <typename T, int DP, bool ALIBI>
+int run_prefill_q8(const Args& a, const PrefillQ8Params& pp, char* msg, size_t msg_len) {
+    constexpr int SMEM = PqCfg<DP, std::is_same<T, __half>::value ? 3 : 2>::SMEM;
+    auto kern = prefill_q8_kernel<T, DP, ALIBI>;
+    static int sms = 0;
+    if (!sms) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        int dev = 0, n = 0;
+        if (e == cudaSuccess) e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (e != cudaSuccess) {
+            snprintf(msg, msg_len, "configuring the q8 prefill (%d bytes of shared memory): %s", SMEM, cudaGetErrorString(e));
+            return PA_ERR_CUDA;
+        }
+        sms = n;
+    }
+    if ((int64_t)pp.pairs * a.Hkv + sms >= (int64_t)INT32_MAX) {
+        snprintf(msg, msg_len, "q8 prefill: %lld work items (tiles x kv heads) exceed the item counter's range",
+                 (long long)pp.pairs * a.Hkv);
+        return PA_ERR_UNSUPPORTED;
+    }
+    const uint64_t dims[4] = {(uint64_t)a.D, (uint64_t)a.Hkv, (uint64_t)a.page, (uint64_t)a.num_blocks};
+    const uint64_t strides[3] = {(uint64_t)a.kv_s2, (uint64_t)a.kv_s1, (uint64_t)a.kv_s0};
+    const uint32_t box[4] = {128u, 1u, (uint32_t)pp.box_rows, 1u};
+    CUtensorMap tk, tv;
+    int rc = encode_tmap_4d(&tk, PA_E4M3, a.k, dims, strides, box, 1, msg, msg_len);
+    if (rc == PA_OK) rc = encode_tmap_4d(&tv, PA_E4M3, a.v, dims, strides, box, 1, msg, msg_len);
+    if (rc != PA_OK) return rc;
+    NvtxRange nv("pa::prefill_q8_kernel");
+    cudaError_t e = cudaMemsetAsync(pp.counter, 0, sizeof(int), a.stream);
+    if (e != cudaSuccess) {
+        snprintf(msg, msg_len, "q8 prefill: zeroing the item counter: %s", cudaGetErrorString(e));
+        return PA_ERR_CUDA;
+    }
+    timer_begin(PA_KC_PREFILL, a.stream);
+    kern<<<std::min(sms, pp.pairs * a.Hkv), kPqThreads, SMEM, a.stream>>>(tk, tv, pp);
+    if ((e = cudaGetLastError()) != cudaSuccess) {
+        snprintf(msg, msg_len, "q8 prefill launch: %s", cudaGetErrorString(e));
+        return PA_ERR_CUDA;
+    }
+    timer_end(PA_KC_PREFILL, a.stream);
+    count_launches(1);
+    return PA_OK;
+}
+
+template <typename T>
+int launch_prefill_q8_t(const Args& a, const PrefillQ8Params& pp, char* msg, size_t msg_len) {
+    if (a.D <= 64)
+        return a.alibi ? run_prefill_q8<T, 64, true>(a, pp, msg, msg_len) : run_prefill_q8<T, 64, false>(a, pp, msg, msg_len);
+    return a.alibi ? run_prefill_q8<T, 128, true>(a, pp, msg, msg_len) : run_prefill_q8<T, 128, false>(a, pp, msg, msg_len);
+}
+
+}  // namespace
+
+// Long queries of these calls go to the kernel above (the same conditions as the 16-bit kernels',
+// up to the head dim).
+bool prefill_q8_supported(const Args& a) { return a.D <= 128 && prefill_supported(a); }
+
+int launch_prefill_q8(const Args& a, int* counter, unsigned int* err, char* msg, size_t msg_len) {
+    if (!counter) {
+        snprintf(msg, msg_len, "the prefill kernels need a device item counter");
+        return PA_ERR_ARG;
+    }
+    PrefillQ8Params pp{};
+    pp.counter = counter;
+    pp.out = a.out;
+    pp.o_s0 = a.o_s0;
+    pp.o_s1 = a.o_s1;
+    pp.lse = a.lse;
+    pp.lse_s0 = a.lse_s0;
+    pp.lse_sb = a.lse_sb;
+    pp.cu_q = a.cu_q;
+    pp.cu_k = a.cu_k;
+    pp.bt = a.block_table;
+    pp.bt_s0 = a.bt_s0;
+    pp.bt_cols = a.bt_cols;
+    pp.batch = a.batch;
+    pp.H = a.H;
+    pp.Hkv = a.Hkv;
+    pp.G = a.H / a.Hkv;
+    pp.D = a.D;
+    pp.P = a.page;
+    pp.num_blocks = a.num_blocks;
+    pp.total_q = a.total_q;
+    pp.paged = 1;
+    pp.max_sq = a.max_sq;
+    pp.max_sk = a.max_sk;
+    pp.scale_log2 = a.scale * 1.4426950408889634f;
+    pp.alibi = a.alibi;
+    pp.wl = a.wl;
+    pp.wr = a.wr;
+    pp.rows_cap = prefill_rows_threshold();
+    pp.err = err;
+    pp.wait_ns = a.wait_ns;
+    pp.withhold = a.withhold_loads;
+    pp.box_rows = a.page % 128 == 0 ? 128 : a.page % 64 == 0 ? 64 : 32;
+    pp.boxes_per_tile = 128 / pp.box_rows;
+    pp.pairs = (int)(prefill_items_bound(a) / a.Hkv);
+    pp.q = a.q;
+    pp.q_s0 = a.q_s0;
+    pp.q_s1 = a.q_s1;
+    pp.ks = a.k_scale;
+    pp.vs = a.v_scale;
+    pp.ks_s0 = a.ks_s0;
+    pp.ks_s1 = a.ks_s1;
+    pp.vs_s0 = a.vs_s0;
+    pp.vs_s1 = a.vs_s1;
+    return a.dtype == PA_BF16 ? launch_prefill_q8_t<__nv_bfloat16>(a, pp, msg, msg_len)
+                              : launch_prefill_q8_t<__half>(a, pp, msg, msg_len);
+}
+
+}  // namespace pa
