@@ -24,7 +24,7 @@
 //   warp 0       takes items and publishes them; K tiles and their scales
 //   warp 2       V tiles
 //   warps 1, 3   MMA issuers of tiles A and B
-//   warps 4..11  softmax, 16 rows (TMEM lanes) of each tile a warp, four threads a row
+//   warps 4..11  softmax, a row (TMEM lane) a thread: 4..7 tile A, 8..11 tile B
 //   warps 12..15 converters: q into its terms at the start of an item, then V tile by tile
 //
 // Tensor-core bound: 4 D flops per (row, key) at the f16 rate (f16 q: 5 D).
@@ -48,8 +48,6 @@ constexpr int kPqRegsControl = 56, kPqRegsSoftmax = 192, kPqRegsConvert = 72;
 constexpr float kPqOffset = 7.f;
 
 struct PrefillQ8Params : PrefillParams {
-    const void* q;
-    int64_t q_s0, q_s1;
     const float* ks;
     const float* vs;
     int64_t ks_s0, ks_s1, vs_s0, vs_s1;
@@ -67,9 +65,9 @@ struct PqCfg {
     static constexpr int OFF_VR = OFF_K + KS * TILE;
     static constexpr int OFF_VC = OFF_VR + VR * TILE;
     static constexpr int OFF_BAR = OFF_VC + 2 * VC_TILE;
-    // q_full, k_full[KS], k_empty[KS], vr_full[VR], vr_empty[VR], vc_full[2], vc_empty[2], s_full[2],
-    // p_full[2], pv_done[2], drain[2], item_ready[2], item_free[2], q_free
-    static constexpr int NBAR = 2 + 2 * KS + 2 * VR + 16;
+    // q_raw[2], q_full[2], q_free[2], k_full[KS], k_empty[KS], vr_full[VR], vr_empty[VR], vc_full[2],
+    // vc_empty[2], s_full[2], p_full[2], pv_done[2], drain[2], item_ready[2], item_free[2]
+    static constexpr int NBAR = 6 + 2 * KS + 2 * VR + 16;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem base, abort flag
     static constexpr int OFF_SLOT = OFF_MISC + 16;       // two item slots
     static constexpr int SC_RING = 8;
@@ -77,16 +75,17 @@ struct PqCfg {
     static constexpr int OFF_EXP = OFF_SC + SC_RING * 48;  // [item parity][tile][row]: e of the row, int8
     static constexpr int SMEM = OFF_EXP + 512 + 1024;
     static constexpr uint32_t T_S0 = 0, T_S1 = 128, T_O0 = 256, T_O1 = 256 + DP;
-    // The scale ring: the K producer writes position g after stage g % KS was released, when every
-    // softmax warp is at tile g - KS - 1 or later, so what it overwrites (g - 8) has been read.
+    // The scale ring: the K producer writes position g after stage g % KS was released, once both
+    // tiles' S of g - KS were seen; S of a tile follows the P of the one before from all its softmax
+    // warps, so each is at g - KS - 1 or later, and what is overwritten (g - 8) has been read.
     static_assert(KS + 1 < SC_RING, "scale ring");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 template <typename T, int DP, bool ALIBI>
 __global__ void __launch_bounds__(kPqThreads, 1)
-    prefill_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                      const PrefillQ8Params p) {
+    prefill_q8_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                      const __grid_constant__ CUtensorMap tm_v, const PrefillQ8Params p) {
     constexpr int NTERM = std::is_same<T, __half>::value ? 3 : 2;
     using C = PqCfg<DP, NTERM>;
     constexpr int KS = C::KS, VR = C::VR;
@@ -94,9 +93,10 @@ __global__ void __launch_bounds__(kPqThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-    uint64_t* q_free = q_full + 1;
-    uint64_t* k_full = q_free + 1;
+    uint64_t* q_raw = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // [tile]: q as loaded
+    uint64_t* q_full = q_raw + 2;   // [tile]: q in its terms
+    uint64_t* q_free = q_full + 2;  // [tile]: the item's Q.K^T products have completed
+    uint64_t* k_full = q_free + 2;
     uint64_t* k_empty = k_full + KS;
     uint64_t* vr_full = k_empty + KS;
     uint64_t* vr_empty = vr_full + VR;
@@ -114,8 +114,6 @@ __global__ void __launch_bounds__(kPqThreads, 1)
     float* sc_ring = reinterpret_cast<float*>(smem + C::OFF_SC);
     int8_t* row_exp = reinterpret_cast<int8_t*>(smem + C::OFF_EXP);
     if (tid == 64) {
-        mbar_init(q_full, 4);  // converter warps
-        mbar_init(q_free, 2);
         for (int s = 0; s < KS; ++s) {
             mbar_init(&k_full[s], 2);   // the copies, the scales
             mbar_init(&k_empty[s], 2);  // one arrive per query tile: the softmax, or issuer B without a tile B
@@ -125,10 +123,13 @@ __global__ void __launch_bounds__(kPqThreads, 1)
             mbar_init(&vr_empty[s], 4);
         }
         for (int x = 0; x < 2; ++x) {
+            mbar_init(&q_raw[x], 1);
+            mbar_init(&q_full[x], 4);  // converter warps
+            mbar_init(&q_free[x], 1);
             mbar_init(&vc_full[x], 4);
             mbar_init(&vc_empty[x], 2);
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 8);
+            mbar_init(&p_full[x], 4);  // softmax warps of the tile
             mbar_init(&pv_done[x], 1);
             mbar_init(&drain[x], 1);
             mbar_init(&item_ready[x], 1);
@@ -311,11 +312,11 @@ __global__ void __launch_bounds__(kPqThreads, 1)
             if (!take_slot(k, it) || it.b < 0) break;
             if (it.bad || it.n_tiles == 0) continue;
             const int n = it.n_tiles;
-            if (!(ok = wait_all(q_full, lq & 1))) break;
+            if (!(ok = wait_all(&q_full[x], lq & 1))) break;
             if (x == 0 || it.has_b) {
                 if (!(ok = wait_all(&k_full[gk % KS], (gk / KS) & 1))) break;
                 issue_s(gk);
-                if (n == 1) tc::commit_elect(q_free);
+                if (n == 1) tc::commit_elect(&q_free[x]);
                 __syncwarp();
                 for (int j = 0; ok && j < n; ++j) {
                     const int g_v = gv + j;
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                     if (j + 1 == n) tc::commit_elect(&pv_done[x]);
                     if (more) {
                         issue_s(g_k);
-                        if (j + 2 == n) tc::commit_elect(q_free);
+                        if (j + 2 == n) tc::commit_elect(&q_free[x]);
                     }
                     __syncwarp();
                 }
@@ -342,7 +343,7 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                 // An item without tile B: this issuer goes through the same phases and releases its
                 // share of q and of every stage.  Were it to skip them, its next wait could meet
                 // a barrier whose phase before that one has yet to complete, and pass at once.
-                if (lane == 0) mbar_arrive(q_free);
+                if (lane == 0) mbar_arrive(&q_free[x]);
                 for (int j = 0; ok && j < n; ++j) {
                     if (!(ok = wait_all(&k_full[(gk + j) % KS], ((gk + j) / KS) & 1))) break;
                     if (lane == 0) mbar_arrive(&k_empty[(gk + j) % KS]);
@@ -367,78 +368,84 @@ __global__ void __launch_bounds__(kPqThreads, 1)
     {
         // ---------------- converters ----------------
         const int cw = warp - 12;
-        const T* q = static_cast<const T*>(p.q);
+        if (cw == 0 && !p.withhold) prefetch_tmap(&tm_q);
         int ld = 0, gv = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
             PfItem it;
             if (!take_slot(k, it) || it.b < 0) break;
             if (it.bad || it.n_tiles == 0) continue;
-            // q, once the previous item's last Q.K^T products have completed: half a warp a row, eight
-            // columns a lane; rows without a query keep what is there (their scores are masked)
-            if (ld >= 1 && !(ok = wait_all(q_free, (ld - 1) & 1))) break;
-            const int half = lane >> 4, u = lane & 15;
-            const int passes = it.has_b ? 32 : 16;
-            for (int p0 = 0; p0 < passes; p0 += 4) {
-                uint4 w[4];
-                bool live[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = (p0 + i) * 8 + cw * 2 + half, rr = r & 127;
-                    const int ql = rr / p.G, qi = it.i0 + (r >> 7) * qpt + ql;
-                    live[i] = rr < trows && qi < it.sq;
-                    w[i] = make_uint4(0, 0, 0, 0);
-                    if (live[i] && u * 8 < p.D)
-                        w[i] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)(it.q0 + qi) * p.q_s0 +
-                                                                    (int64_t)(it.hk * p.G + rr - ql * p.G) * p.q_s1 + u * 8));
+            // q: tile x is loaded over the terms of the item before once its last Q.K^T products have
+            // completed (a step before the item ends: the load and the conversion run beside its
+            // last softmax and its epilogue), the 128-byte chunks of a row into that row of terms 0
+            // and 1, and converted in place, DP / 8 lanes a row.
+            for (int x = 0; ok && x < 2; ++x) {
+                if (ld >= 1 && !(ok = wait_all(&q_free[x], (ld - 1) & 1))) break;
+                if (cw == 0 && lane == 0 && !p.withhold) {
+                    if (x == 0 || it.has_b) {
+                        mbar_arrive_expect_tx(&q_raw[x], (DP / 64) * trows * 128);
+                        for (int c = 0; c < DP / 64; ++c)
+                            tma_load_4d(smem + C::OFF_Q + (x * NTERM + c) * C::TILE, &tm_q, &q_raw[x], c * 64, it.hk * p.G,
+                                        it.q0 + it.i0 + x * qpt, 0, 0ull);
+                    } else {
+                        mbar_arrive(&q_raw[x]);
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = (p0 + i) * 8 + cw * 2 + half, rr = r & 127;
-                    float y[8];
-                    const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-                    float mx = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = unpack2<T>(ww[e]);
-                        y[2 * e] = f.x;
-                        y[2 * e + 1] = f.y;
-                        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
-#pragma unroll
-                    for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                    // the largest power of two with mx 2^e2 <= 448 = 1.75 x 2^8
-                    const int bits = __float_as_int(mx);
-                    const int e2 = min(126, 8 - ((bits >> 23) - 127) - ((bits & 0x7fffff) > 0x600000 ? 1 : 0));
-                    const float up = __int_as_float((127 + e2) << 23);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        y[e] *= up;
-                        if (!(fabsf(y[e]) <= FLT_MAX)) y[e] = NAN;  // the row's scores become NaN
-                    }
-                    uint8_t* dst = smem + C::OFF_Q + (r >> 7) * (NTERM * C::TILE) + rr * 128 + (((u >> 1) ^ (rr & 7)) << 4) +
-                                   (u & 1) * 8;
-#pragma unroll
-                    for (int t = 0; t < NTERM; ++t) {
-                        uint32_t c2[4];
+                __syncwarp();
+            }
+            for (int x = 0; ok && x < 2; ++x) {
+                if (!(ok = wait_all(&q_raw[x], ld & 1))) break;
+                if (x == 0 || it.has_b) {
+                    constexpr int LPR = DP / 8, RPP = 32 / LPR;  // lanes of a row, rows of a pass
+                    const int u = lane % LPR;
+                    uint8_t* tile = smem + C::OFF_Q + x * (NTERM * C::TILE);
+#pragma unroll 4
+                    for (int i = 0; i < 32 / RPP; ++i) {
+                        const int r = cw * 32 + i * RPP + lane / LPR;
+                        const uint4 w = *reinterpret_cast<const uint4*>(tile + (u >> 3) * C::TILE + swz128(r, u & 7));
+                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                        float y[8], mx = 0.f;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            c2[e] = e4m3x2(y[2 * e], y[2 * e + 1]);
-                            if (t + 1 < NTERM) {
-                                const float2 f = unpack2<__half>(e4m3x2_to_half2(c2[e]));
-                                y[2 * e] -= f.x;
-                                y[2 * e + 1] -= f.y;
-                            }
+                            const float2 f = unpack2<T>(ww[e]);
+                            y[2 * e] = f.x;
+                            y[2 * e + 1] = f.y;
+                            mx = max3f(mx, fabsf(f.x), fabsf(f.y));
                         }
-                        if (live[i])
-                            *reinterpret_cast<uint2*>(dst + t * C::TILE) = make_uint2(c2[0] | (c2[1] << 16), c2[2] | (c2[3] << 16));
+#pragma unroll
+                        for (int off = LPR / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                        // the largest power of two with mx 2^e2 <= 448 = 1.75 x 2^8
+                        const int bits = __float_as_int(mx);
+                        const int e2 = min(126, 8 - ((bits >> 23) - 127) - ((bits & 0x7fffff) > 0x600000 ? 1 : 0));
+                        const float up = __int_as_float((127 + e2) << 23);
+                        // (a row with an infinite element becomes NaN, and so do its scores)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) y[e] = mx <= FLT_MAX ? y[e] * up : NAN;
+                        uint8_t* dst = tile + swz128(r, u >> 1) + (u & 1) * 8;
+#pragma unroll
+                        for (int t = 0; t < NTERM; ++t) {
+                            uint32_t c2[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                c2[e] = e4m3x2(y[2 * e], y[2 * e + 1]);
+                                if (t + 1 < NTERM) {
+                                    const float2 f = unpack2<__half>(e4m3x2_to_half2(c2[e]));
+                                    y[2 * e] -= f.x;
+                                    y[2 * e + 1] -= f.y;
+                                }
+                            }
+                            if (t == 0) __syncwarp();  // every lane of the row has read its columns
+                            *reinterpret_cast<uint2*>(dst + t * C::TILE) =
+                                make_uint2(c2[0] | (c2[1] << 16), c2[2] | (c2[3] << 16));
+                        }
+                        if (u == 0) row_exp[(ld & 1) * 256 + x * 128 + r] = (int8_t)e2;
                     }
-                    if (u == 0) row_exp[(ld & 1) * 256 + r] = (int8_t)e2;
                 }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[x]);
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
+            if (!ok) break;
             // V tiles: warp cw converts rows 32 cw .. + 31
             const int64_t cdiag = (int64_t)it.sk - it.sq;
             const int i_last = min(it.sq - 1, it.i0 + (it.has_b ? 2 : 1) * qpt - 1);
@@ -491,276 +498,171 @@ __global__ void __launch_bounds__(kPqThreads, 1)
     } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPqRegsSoftmax));
     {
-        // ---------------- softmax: tile A and then tile B at every key tile ----------------
-        // Warp w takes TMEM lanes lb .. lb + 15, thread t rows lb + t/4 (q = 0) and + 8 (q = 1), keys
-        // 8 k + 2 (t % 4) + {0, 1}; k / 4 is the 32-key group, whose scales are its page's.
-        const int lg = warp & 3, hh = (warp - 4) >> 2;
-        const int gid = lane >> 2, tig = lane & 3;
-        const int lb = lg * 32 + hh * 16;
-        const uint32_t lane_addr = (uint32_t)lb << 16;
+        // ---------------- softmax: warps 4..7 for tile A, 8..11 for tile B ----------------
+        // Thread t of warp w holds row (TMEM lane) 32 (w % 4) + t with all 128 keys of a tile, so a row
+        // needs no exchange, and the two warps of a scheduler, one of each tile, are at different
+        // points of their steps: one's exponentials run under the other's loads and waits.  (All
+        // eight warps on tile A and then on tile B, two rows and 64 keys of each a thread, as in
+        // prefill_kernel: 1,793 us on eight prompts of 1024..8192 tokens.)
+        const int x = (warp - 4) >> 2;
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_addr = tmem + lane_addr + (x ? C::T_S1 : C::T_S0);
+        const uint32_t o_addr = tmem + lane_addr + (x ? C::T_O1 : C::T_O0);
         T* out = static_cast<T*>(p.out);
-        struct TileRows {
-            int lo[2], hi[2];
-            float m[2], l[2], sl[2];
-            int dg[2];
-            float ab[2];
-        };
-        int qi[2], gi[2];
-        bool pad[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const int r = lb + gid + 8 * q;
-            qi[q] = r / p.G;
-            gi[q] = r - qi[q] * p.G;
-            pad[q] = r >= trows;
-        }
-        int gk = 0, gv = 0, sa = 0, sb = 0, aa = 0, ab_ = 0, ld = 0;
+        const int qi = row / p.G, gi = row - qi * p.G;  // query of the tile, head of the group
+        const bool pad = row >= trows;
+        int gk = 0, gv = 0, sx = 0, px = 0, ld = 0;
         bool ok = true;
         for (int k = 0; ok; ++k) {
             PfItem it;
             if (!take_slot(k, it) || it.b < 0) break;
             if (it.bad) continue;
-            const int b = it.b, hk = it.hk;
-            const int64_t cdiag = (int64_t)it.sk - it.sq;
-            const int64_t rows_total = (int64_t)it.sq * p.G;
+            const int qrow = it.i0 + x * qpt + qi;  // query of the sequence
+            const bool live = !pad && qrow < it.sq;
+            const int h = it.hk * p.G + gi;
+            const int64_t t_row = (int64_t)it.q0 + qrow;
+            T* orow = out + t_row * p.o_s0 + (int64_t)h * p.o_s1;
+            float* lse = p.lse + (int64_t)h * p.lse_s0 + t_row + (int64_t)it.b * p.lse_sb;
             if (it.n_tiles == 0) {  // no row attends any key: out = 0, lse = -inf
-                const int x = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
-                const int64_t rho = (int64_t)(it.i0 + x * qpt) * p.G + r;
-                if (r < trows && rho < rows_total) {
-                    const int i = (int)(rho / p.G), g = (int)(rho - (int64_t)i * p.G);
-                    const int64_t t = it.q0 + i;
-                    const int h = hk * p.G + g;
-                    for (int d = 0; d < p.D; d += 8)
-                        *reinterpret_cast<int4*>(out + t * p.o_s0 + (int64_t)h * p.o_s1 + d) = make_int4(0, 0, 0, 0);
-                    p.lse[(int64_t)h * p.lse_s0 + t + (int64_t)b * p.lse_sb] = -INFINITY;
+                if (live) {
+                    for (int d = 0; d < p.D; d += 8) *reinterpret_cast<int4*>(orow + d) = make_int4(0, 0, 0, 0);
+                    *lse = -INFINITY;
                 }
                 continue;
             }
             const int n = it.n_tiles;
-            auto qrow = [&](int x, int q) { return it.i0 + x * qpt + qi[q]; };
-            auto live = [&](int x, int q) { return !pad[q] && qrow(x, q) < it.sq; };
-            auto init_rows = [&](int x, TileRows& st) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    st.lo[q] = 0;
-                    st.hi[q] = -1;
-                    st.dg[q] = 0;
-                    st.ab[q] = 0.f;
-                    if (live(x, q)) {
-                        const int64_t diag = qrow(x, q) + cdiag;
-                        st.lo[q] = p.wl >= 0 ? (int)max64(0, diag - p.wl) : 0;
-                        st.hi[q] = p.wr >= 0 ? (int)max64(-1, min64((int64_t)it.sk - 1, diag + p.wr)) : it.sk - 1;
-                        if (ALIBI) {
-                            st.dg[q] = (int)diag;
-                            st.ab[q] = p.alibi[hk * p.G + gi[q]] * kLog2e;
-                        }
-                    }
-                    st.m[q] = -INFINITY;
-                    st.l[q] = 0.f;
-                    st.sl[q] = 0.f;
-                }
-            };
-            TileRows rows_a, rows_b;
-            init_rows(0, rows_a);
-            init_rows(1, rows_b);
+            if (x == 1 && !it.has_b) {
+                gk += n;
+                gv += n;
+                ++ld;
+                continue;
+            }
+            const int64_t diag = qrow + ((int64_t)it.sk - it.sq);
+            const int lo = p.wl >= 0 ? (int)max64(0, diag - p.wl) : 0;
+            const int hi = !live ? -1 : p.wr >= 0 ? (int)max64(-1, min64((int64_t)it.sk - 1, diag + p.wr)) : it.sk - 1;
+            const float ab = ALIBI && live ? p.alibi[h] * kLog2e : 0.f;
+            float m = -INFINITY, l = 0.f, sl = 0.f;
 
-            auto step = [&](int x, TileRows& st, int j) -> bool {
+            // One key tile: S -> running reference -> (rare) O rescale -> P.
+            auto step = [&](int j) -> bool {
                 const int kt = it.kt0 + j * 128;
-                const int sc = (x ? sb : sa) + j;
-                if (!__all_sync(0xffffffffu, wait_bar(&s_full[x], sc & 1, abort_flag, p.err, p.wait_ns))) return false;
+                if (!__all_sync(0xffffffffu, wait_bar(&s_full[x], (sx + j) & 1, abort_flag, p.err, p.wait_ns))) return false;
                 tc::fence_after_sync();
-                const uint32_t s_addr = tmem + lane_addr + (x ? C::T_S1 : C::T_S0);
-                const uint32_t o_addr = tmem + lane_addr + (x ? C::T_O1 : C::T_O0);
-                float sv[64];
-                tc::ld_16x256b_x8(s_addr, *reinterpret_cast<float(*)[32]>(&sv[0]));
-                tc::ld_16x256b_x8(s_addr + 64, *reinterpret_cast<float(*)[32]>(&sv[32]));
-                if (warp == 4 && lane == 0) {
+                float sv[4][32];  // by 32-key group
+#pragma unroll
+                for (int g = 0; g < 4; ++g) tc::ld_32cols(s_addr + 32 * g, sv[g]);
+                // scales of the groups, while S is on its way
+                const float4* slot = reinterpret_cast<const float4*>(sc_ring + ((gk + j) % C::SC_RING) * 12);
+                const float4 ks4 = slot[0], lv4 = slot[1], inv4 = slot[2];
+                if (j == 0) sl = p.scale_log2 * __int_as_float((127 - row_exp[(ld & 1) * 256 + x * 128 + row]) << 23);
+                float c[4] = {sl * ks4.x, sl * ks4.y, sl * ks4.z, sl * ks4.w};
+                const float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, inv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
+                tc::wait_ld();
+                if ((warp & 3) == 0 && lane == 0) {
                     mbar_arrive(&k_empty[(gk + j) % KS]);
                     if (j > 0) mbar_arrive(&vc_empty[(gv + j - 1) & 1]);
                 }
-                // scales of the four 32-key groups; c[q][g] > 0 so that -inf x c stays -inf
-                const float* slot = sc_ring + ((gk + j) % C::SC_RING) * 12;
-                float c[2][4], lv[4];
-                if (j == 0) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const int e = row_exp[(ld & 1) * 256 + x * 128 + lb + gid + 8 * q];
-                        st.sl[q] = p.scale_log2 * __int_as_float((127 - e) << 23);
-                    }
-                }
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float ksg = slot[g];
-                    lv[g] = slot[4 + g];
-                    c[0][g] = fmaxf(st.sl[0] * ksg, 1e-37f);
-                    c[1][g] = fmaxf(st.sl[1] * ksg, 1e-37f);
-                }
-                tc::wait_ld();
-                if (!(kt >= max(st.lo[0], st.lo[1]) && kt + 127 <= min(st.hi[0], st.hi[1]))) {
-#pragma unroll
-                    for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-                        for (int q = 0; q < 2; ++q)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int key = kt + 8 * kk + 2 * tig + e;
-                                float& v = sv[4 * kk + 2 * q + e];
-                                v = (key >= st.lo[q] && key <= st.hi[q]) ? v : -INFINITY;
-                            }
-                }
-                if (ALIBI) {  // the whole x here: c = 1 and log2 vs = 0 below
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float d0 = (float)(st.dg[q] - kt - 2 * tig);
-#pragma unroll
-                        for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float& v = sv[4 * kk + 2 * q + e];
-                                v = fmaf(-st.ab[q], fabsf(d0 - (float)(8 * kk + e)), fmaf(v, c[q][kk >> 2], lv[kk >> 2]));
-                            }
-                    }
-                }
-                float lm[2];
-                bool grow = false;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    lm[q] = -INFINITY;
+                if (kt < lo || kt + 127 > hi) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const float* v = &sv[16 * g + 2 * q];
-                        float t = fmaxf(v[0], v[1]);
+                        c[g] = fmaxf(c[g], 1e-37f);  // a scale of 0 keeps -inf x c at -inf
 #pragma unroll
-                        for (int kk = 1; kk < 4; ++kk) t = max3f(t, v[4 * kk], v[4 * kk + 1]);
-                        lm[q] = fmaxf(lm[q], ALIBI ? t : fmaf(t, c[q][g], lv[g]));
-                    }
-                    grow |= lm[q] > st.m[q] + 8.f;
-                }
-                float alpha[2] = {1.f, 1.f};
-                if (__any_sync(0xffffffffu, grow)) {
-                    bool resc = false;
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float mx = lm[q];
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        if (mx > st.m[q] + 8.f) {
-                            alpha[q] = fast_exp2(st.m[q] - mx);
-                            st.m[q] = mx;
-                            resc = true;
-                        }
-                    }
-                    // O_x's last P.V (PV_x(j-1)) precedes S_x(j) on its issuer: complete now
-                    if (j > 0 && __any_sync(0xffffffffu, resc)) {
-#pragma unroll 1
-                        for (int cc = 0; cc < DP / 64; ++cc) {
-                            float o[32];
-                            tc::ld_16x256b_x8(o_addr + cc * 64, o);
-                            tc::wait_ld();
-                            uint32_t ob[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) ob[e] = __float_as_uint(o[e] * alpha[(e >> 1) & 1]);
-                            tc::st_16x256b_x8(o_addr + cc * 64, ob);
+                        for (int i = 0; i < 32; ++i) {
+                            const int key = kt + 32 * g + i;
+                            sv[g][i] = key >= lo && key <= hi ? sv[g][i] : -INFINITY;
                         }
                     }
                 }
-                float nm[2];
+                if (ALIBI) {  // the whole x here: c = 1 and log2 vs = 0 below
+                    const float d0 = (float)((int)diag - kt);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    nm[q] = st.m[q] == -INFINITY ? 0.f : kPqOffset - st.m[q];
-                    st.l[q] *= alpha[q];
+                    for (int g = 0; g < 4; ++g)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            sv[g][i] = fmaf(-ab, fabsf(d0 - (float)(32 * g + i)), fmaf(sv[g][i], c[g], lv[g]));
                 }
-                uint32_t pk[32];
+                float mx = -INFINITY;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const float inv = slot[8 + g];
+                    float t0 = fmaxf(sv[g][0], sv[g][1]), t1 = fmaxf(sv[g][2], sv[g][3]);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const float cg = ALIBI ? 1.f : c[q][g], ag = ALIBI ? nm[q] : nm[q] + lv[g];
-                        float s0 = 0.f, s1 = 0.f;
+                    for (int i = 4; i < 32; i += 4) {
+                        t0 = max3f(t0, sv[g][i], sv[g][i + 1]);
+                        t1 = max3f(t1, sv[g][i + 2], sv[g][i + 3]);
+                    }
+                    t0 = fmaxf(t0, t1);
+                    mx = fmaxf(mx, ALIBI ? t0 : fmaf(t0, c[g], lv[g]));
+                }
+                const bool grow = mx > m + 8.f;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float alpha = grow ? fast_exp2(m - mx) : 1.f;
+                    if (grow) m = mx;
+                    l *= alpha;
+                    // the tile's last P.V precedes S(j) on its issuer: complete now
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int cc = 0; cc < DP / 16; ++cc) {
+                            uint32_t o[16];
+                            tc::ld_32x32b_x16(o_addr + cc * 16, o);
+                            tc::wait_ld();
 #pragma unroll
-                        for (int k4 = 0; k4 < 4; ++k4) {
-                            const int kk = 4 * g + k4;
-                            float x0, x1;
-                            ffma2(x0, x1, sv[4 * kk + 2 * q], sv[4 * kk + 2 * q + 1], cg, cg, ag, ag);
-                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                            fadd2_acc(s0, s1, p0, p1);
-                            pk[2 * kk + q] = pack2<__half>(p0, p1);
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                            tc::st_32x32b_x16(o_addr + cc * 16, o);
                         }
-                        st.l[q] = fmaf(s0 + s1, inv, st.l[q]);
                     }
                 }
-                tc::st_16x128b_x16(s_addr, pk);
+                const float nm = m == -INFINITY ? 0.f : kPqOffset - m;
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const float cg = ALIBI ? 1.f : c[g], ag = ALIBI ? nm : nm + lv[g];
+                    float s0 = 0.f, s1 = 0.f;
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x0, x1;
+                        ffma2(x0, x1, sv[g][2 * i], sv[g][2 * i + 1], cg, cg, ag, ag);
+                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                        fadd2_acc(s0, s1, p0, p1);
+                        pk[i] = pack2<__half>(p0, p1);
+                    }
+                    l = fmaf(s0 + s1, inv[g], l);
+                    tc::st_32x32b_x16(s_addr + 16 * g, pk);
+                }
                 tc::wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[x]);
                 return true;
             };
-
-            auto epilogue = [&](int x, TileRows& st) -> bool {
-                if (!__all_sync(0xffffffffu,
-                                wait_bar(&pv_done[x], (x ? ab_ : aa) & 1, abort_flag, p.err, p.wait_ns)))
-                    return false;
-                tc::fence_after_sync();
-                if (warp == 4 && lane == 0) mbar_arrive(&vc_empty[(gv + n - 1) & 1]);
-                const uint32_t o_addr = tmem + lane_addr + (x ? C::T_O1 : C::T_O0);
-                float inv[2];
-                T* orow[2];
-                bool valid[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float l = st.l[q];
-                    l += __shfl_xor_sync(0xffffffffu, l, 1);
-                    l += __shfl_xor_sync(0xffffffffu, l, 2);
-                    inv[q] = l == 0.f ? 0.f : 1.f / l;
-                    valid[q] = live(x, q);
-                    const int64_t t = it.q0 + qrow(x, q);
-                    const int h = hk * p.G + gi[q];
-                    orow[q] = out + t * p.o_s0 + (int64_t)h * p.o_s1;
-                    if (valid[q] && tig == 0)
-                        p.lse[(int64_t)h * p.lse_s0 + t + (int64_t)b * p.lse_sb] =
-                            l == 0.f ? -INFINITY : (st.m[q] - kPqOffset + log2f(l)) * 0.69314718055994531f;
-                }
-                // a 4 x 4 transpose over each quad: two 16-byte stores per row and 64-column chunk
 #pragma unroll 1
-                for (int cc = 0; cc < DP / 64; ++cc) {
+            for (int j = 0; ok && j < n; ++j) ok = step(j);
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&pv_done[x], px & 1, abort_flag, p.err, p.wait_ns));
+            if (ok) {
+                tc::fence_after_sync();
+                if ((warp & 3) == 0 && lane == 0) mbar_arrive(&vc_empty[(gv + n - 1) & 1]);
+                const float inv_l = l == 0.f ? 0.f : 1.f / l;
+                if (live) *lse = l == 0.f ? -INFINITY : (m - kPqOffset + log2f(l)) * 0.69314718055994531f;
+#pragma unroll 1
+                for (int cc = 0; cc < DP / 32; ++cc) {  // 64 bytes of the row a pass
                     float o[32];
-                    tc::ld_16x256b_x8(o_addr + cc * 64, o);
+                    tc::ld_32cols(o_addr + cc * 32, o);
                     tc::wait_ld();
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            w[kk] = pack2<T>(o[4 * kk + 2 * q] * inv[q], o[4 * kk + 2 * q + 1] * inv[q]);
-                        quad_transpose(*reinterpret_cast<uint32_t(*)[4]>(&w[0]), tig);
-                        quad_transpose(*reinterpret_cast<uint32_t(*)[4]>(&w[4]), tig);
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const int d = cc * 64 + 32 * hf + 8 * tig;
-                            if (valid[q] && d < p.D)
-                                *reinterpret_cast<uint4*>(orow[q] + d) =
-                                    make_uint4(w[4 * hf], w[4 * hf + 1], w[4 * hf + 2], w[4 * hf + 3]);
-                        }
+                    for (int v = 0; v < 4; ++v) {
+                        const int d = cc * 32 + v * 8;
+                        if (live && d < p.D)
+                            *reinterpret_cast<uint4*>(orow + d) =
+                                make_uint4(pack2<T>(o[8 * v] * inv_l, o[8 * v + 1] * inv_l),
+                                           pack2<T>(o[8 * v + 2] * inv_l, o[8 * v + 3] * inv_l),
+                                           pack2<T>(o[8 * v + 4] * inv_l, o[8 * v + 5] * inv_l),
+                                           pack2<T>(o[8 * v + 6] * inv_l, o[8 * v + 7] * inv_l));
                     }
                 }
                 tc::fence_before_sync();  // before this warp's next arrival on p_full[x]
-                return true;
-            };
-
-            for (int j = 0; ok && j < n; ++j) {
-                ok = step(0, rows_a, j);
-                if (ok && it.has_b) ok = step(1, rows_b, j);
             }
-            if (ok) ok = epilogue(0, rows_a);
-            if (ok && it.has_b) ok = epilogue(1, rows_b);
-            sa += n;
-            ++aa;
-            if (it.has_b) {
-                sb += n;
-                ++ab_;
-            }
+            sx += n;
+            ++px;
             gk += n;
             gv += n;
             ++ld;
@@ -800,8 +702,12 @@ int run_prefill_q8(const Args& a, const PrefillQ8Params& pp, char* msg, size_t m
     const uint64_t dims[4] = {(uint64_t)a.D, (uint64_t)a.Hkv, (uint64_t)a.page, (uint64_t)a.num_blocks};
     const uint64_t strides[3] = {(uint64_t)a.kv_s2, (uint64_t)a.kv_s1, (uint64_t)a.kv_s0};
     const uint32_t box[4] = {128u, 1u, (uint32_t)pp.box_rows, 1u};
-    CUtensorMap tk, tv;
-    int rc = encode_tmap_4d(&tk, PA_E4M3, a.k, dims, strides, box, 1, msg, msg_len);
+    const uint64_t qdims[4] = {(uint64_t)a.D, (uint64_t)a.H, (uint64_t)a.total_q, 1};
+    const uint64_t qstrides[3] = {(uint64_t)a.q_s1 * 2, (uint64_t)a.q_s0 * 2, (uint64_t)a.q_s0 * 2 * a.total_q};
+    const uint32_t qbox[4] = {64u, (uint32_t)pp.G, (uint32_t)(128 / pp.G), 1u};
+    CUtensorMap tq, tk, tv;
+    int rc = encode_tmap_4d(&tq, a.dtype, a.q, qdims, qstrides, qbox, 1, msg, msg_len);
+    if (rc == PA_OK) rc = encode_tmap_4d(&tk, PA_E4M3, a.k, dims, strides, box, 1, msg, msg_len);
     if (rc == PA_OK) rc = encode_tmap_4d(&tv, PA_E4M3, a.v, dims, strides, box, 1, msg, msg_len);
     if (rc != PA_OK) return rc;
     NvtxRange nv("pa::prefill_q8_kernel");
@@ -811,7 +717,7 @@ int run_prefill_q8(const Args& a, const PrefillQ8Params& pp, char* msg, size_t m
         return PA_ERR_CUDA;
     }
     timer_begin(PA_KC_PREFILL, a.stream);
-    kern<<<std::min(sms, pp.pairs * a.Hkv), kPqThreads, SMEM, a.stream>>>(tk, tv, pp);
+    kern<<<std::min(sms, pp.pairs * a.Hkv), kPqThreads, SMEM, a.stream>>>(tq, tk, tv, pp);
     if ((e = cudaGetLastError()) != cudaSuccess) {
         snprintf(msg, msg_len, "q8 prefill launch: %s", cudaGetErrorString(e));
         return PA_ERR_CUDA;
@@ -874,9 +780,6 @@ int launch_prefill_q8(const Args& a, int* counter, unsigned int* err, char* msg,
     pp.box_rows = a.page % 128 == 0 ? 128 : a.page % 64 == 0 ? 64 : 32;
     pp.boxes_per_tile = 128 / pp.box_rows;
     pp.pairs = (int)(prefill_items_bound(a) / a.Hkv);
-    pp.q = a.q;
-    pp.q_s0 = a.q_s0;
-    pp.q_s1 = a.q_s1;
     pp.ks = a.k_scale;
     pp.vs = a.v_scale;
     pp.ks_s0 = a.ks_s0;
