@@ -42,9 +42,9 @@ namespace pa {
 namespace {
 
 constexpr int kPqThreads = 512;
-// Register split (setmaxnreg) of the launch's 512 x 128: control 56, softmax 192, converters 72:
-// 128 x 56 + 256 x 192 + 128 x 72 = 65,536.
-constexpr int kPqRegsControl = 56, kPqRegsSoftmax = 192, kPqRegsConvert = 72;
+// Register split (setmaxnreg) of the launch's 512 x 128: control 96, softmax 152, converters 112:
+// 128 x 96 + 256 x 152 + 128 x 112 = 65,536.  (56 / 192 / 72 spilled in the issuers: 7 % slower.)
+constexpr int kPqRegsControl = 96, kPqRegsSoftmax = 152, kPqRegsConvert = 112;
 constexpr float kPqOffset = 7.f;
 
 struct PrefillQ8Params : PrefillParams {
@@ -399,46 +399,60 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                     constexpr int LPR = DP / 8, RPP = 32 / LPR;  // lanes of a row, rows of a pass
                     const int u = lane % LPR;
                     uint8_t* tile = smem + C::OFF_Q + x * (NTERM * C::TILE);
-#pragma unroll 4
-                    for (int i = 0; i < 32 / RPP; ++i) {
-                        const int r = cw * 32 + i * RPP + lane / LPR;
-                        const uint4 w = *reinterpret_cast<const uint4*>(tile + (u >> 3) * C::TILE + swz128(r, u & 7));
-                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-                        float y[8], mx = 0.f;
+                    constexpr int NB = 2;  // rows of a lane whose chains of shuffles and roundings overlap
+#pragma unroll 1
+                    for (int i0 = 0; i0 < 32 / RPP; i0 += NB) {
+                        uint4 w[NB];
+                        float mx[NB];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float2 f = unpack2<T>(ww[e]);
-                            y[2 * e] = f.x;
-                            y[2 * e + 1] = f.y;
-                            mx = max3f(mx, fabsf(f.x), fabsf(f.y));
+                        for (int i = 0; i < NB; ++i) {
+                            const int r = cw * 32 + (i0 + i) * RPP + lane / LPR;
+                            w[i] = *reinterpret_cast<const uint4*>(tile + (u >> 3) * C::TILE + swz128(r, u & 7));
                         }
 #pragma unroll
-                        for (int off = LPR / 2; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                        // the largest power of two with mx 2^e2 <= 448 = 1.75 x 2^8
-                        const int bits = __float_as_int(mx);
-                        const int e2 = min(126, 8 - ((bits >> 23) - 127) - ((bits & 0x7fffff) > 0x600000 ? 1 : 0));
-                        const float up = __int_as_float((127 + e2) << 23);
-                        // (a row with an infinite element becomes NaN, and so do its scores)
+                        for (int i = 0; i < NB; ++i) {
+                            const float2 f0 = unpack2<T>(w[i].x), f1 = unpack2<T>(w[i].y), f2 = unpack2<T>(w[i].z),
+                                         f3 = unpack2<T>(w[i].w);
+                            mx[i] = max3f(max3f(fabsf(f0.x), fabsf(f0.y), fabsf(f1.x)),
+                                          max3f(fabsf(f1.y), fabsf(f2.x), fabsf(f2.y)), fmaxf(fabsf(f3.x), fabsf(f3.y)));
+                        }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) y[e] = mx <= FLT_MAX ? y[e] * up : NAN;
-                        uint8_t* dst = tile + swz128(r, u >> 1) + (u & 1) * 8;
+                        for (int off = LPR / 2; off > 0; off >>= 1)
 #pragma unroll
-                        for (int t = 0; t < NTERM; ++t) {
-                            uint32_t c2[4];
+                            for (int i = 0; i < NB; ++i) mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], off));
+                        __syncwarp();  // every lane of these rows has read its columns
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) {
+                            const int r = cw * 32 + (i0 + i) * RPP + lane / LPR;
+                            // the largest power of two with mx 2^e2 <= 448 = 1.75 x 2^8
+                            const int bits = __float_as_int(mx[i]);
+                            const int e2 = min(126, 8 - ((bits >> 23) - 127) - ((bits & 0x7fffff) > 0x600000 ? 1 : 0));
+                            // (a row with an infinite element becomes NaN, and so do its scores)
+                            const float up = mx[i] <= FLT_MAX ? __int_as_float((127 + e2) << 23) : NAN;
+                            const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                            uint32_t c2[NTERM][4];
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                c2[e] = e4m3x2(y[2 * e], y[2 * e + 1]);
-                                if (t + 1 < NTERM) {
-                                    const float2 f = unpack2<__half>(e4m3x2_to_half2(c2[e]));
-                                    y[2 * e] -= f.x;
-                                    y[2 * e + 1] -= f.y;
+                                float2 y = unpack2<T>(ww[e]);
+                                y.x *= up;
+                                y.y *= up;
+#pragma unroll
+                                for (int t = 0; t < NTERM; ++t) {
+                                    c2[t][e] = e4m3x2(y.x, y.y);
+                                    if (t + 1 < NTERM) {
+                                        const float2 f = unpack2<__half>(e4m3x2_to_half2(c2[t][e]));
+                                        y.x -= f.x;
+                                        y.y -= f.y;
+                                    }
                                 }
                             }
-                            if (t == 0) __syncwarp();  // every lane of the row has read its columns
-                            *reinterpret_cast<uint2*>(dst + t * C::TILE) =
-                                make_uint2(c2[0] | (c2[1] << 16), c2[2] | (c2[3] << 16));
+                            uint8_t* dst = tile + swz128(r, u >> 1) + (u & 1) * 8;
+#pragma unroll
+                            for (int t = 0; t < NTERM; ++t)
+                                *reinterpret_cast<uint2*>(dst + t * C::TILE) =
+                                    make_uint2(c2[t][0] | (c2[t][1] << 16), c2[t][2] | (c2[t][3] << 16));
+                            if (u == 0) row_exp[(ld & 1) * 256 + x * 128 + r] = (int8_t)e2;
                         }
-                        if (u == 0) row_exp[(ld & 1) * 256 + x * 128 + r] = (int8_t)e2;
                     }
                 }
                 fence_proxy_async_smem();
@@ -461,7 +475,10 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                 constexpr int UPR = DP / 16;          // 16-byte units of a row
                 constexpr int RPP = 32 / UPR;         // rows a warp converts a pass
                 const int uu = lane % UPR;
-#pragma unroll 4
+                uint8_t* d = dst + (uu >> 2) * C::TILE;
+                const int u0 = (uu & 3) * 2;
+                const bool sw = (uu & 4) != 0;
+#pragma unroll 1
                 for (int i = 0; i < 32 / RPP; ++i) {
                     const int r = cw * 32 + i * RPP + lane / UPR;
                     uint4 v = *reinterpret_cast<const uint4*>(src + swz128(r, uu));
@@ -475,11 +492,6 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                     b.y = e4m3x2_hi_to_half2(v.z);
                     b.z = e4m3x2_to_half2(v.w);
                     b.w = e4m3x2_hi_to_half2(v.w);
-                    // two 16-byte units of 64-column chunk uu / 4; the lanes of the second chunk, whose
-                    // rows share the first's banks, write theirs in the other order
-                    uint8_t* d = dst + (uu >> 2) * C::TILE;
-                    const int u0 = (uu & 3) * 2;
-                    const bool sw = (uu & 4) != 0;
                     *reinterpret_cast<uint4*>(d + swz128(r, u0 + (sw ? 1 : 0))) = sw ? b : a;
                     *reinterpret_cast<uint4*>(d + swz128(r, u0 + (sw ? 0 : 1))) = sw ? a : b;
                 }
@@ -501,9 +513,10 @@ __global__ void __launch_bounds__(kPqThreads, 1)
         // ---------------- softmax: warps 4..7 for tile A, 8..11 for tile B ----------------
         // Thread t of warp w holds row (TMEM lane) 32 (w % 4) + t with all 128 keys of a tile, so a row
         // needs no exchange, and the two warps of a scheduler, one of each tile, are at different
-        // points of their steps: one's exponentials run under the other's loads and waits.  (All
-        // eight warps on tile A and then on tile B, two rows and 64 keys of each a thread, as in
-        // prefill_kernel: 1,793 us on eight prompts of 1024..8192 tokens.)
+        // points of their steps: one's exponentials run under the other's loads and waits.  On eight
+        // prompts of 1024..8192 tokens: 1,596 us; with all eight warps on tile A and then on tile B, two
+        // rows and 64 keys of each a thread, as in prefill_kernel, 1,793; with sixteen warps, half a row a
+        // thread, 1,750.
         const int x = (warp - 4) >> 2;
         const int row = (warp & 3) * 32 + lane;
         const uint32_t lane_addr = (uint32_t)((warp & 3) * 32) << 16;
@@ -549,50 +562,63 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                 const int kt = it.kt0 + j * 128;
                 if (!__all_sync(0xffffffffu, wait_bar(&s_full[x], (sx + j) & 1, abort_flag, p.err, p.wait_ns))) return false;
                 tc::fence_after_sync();
-                float sv[4][32];  // by 32-key group
-#pragma unroll
-                for (int g = 0; g < 4; ++g) tc::ld_32cols(s_addr + 32 * g, sv[g]);
-                // scales of the groups, while S is on its way
-                const float4* slot = reinterpret_cast<const float4*>(sc_ring + ((gk + j) % C::SC_RING) * 12);
-                const float4 ks4 = slot[0], lv4 = slot[1], inv4 = slot[2];
+                const float* slot = sc_ring + ((gk + j) % C::SC_RING) * 12;
                 if (j == 0) sl = p.scale_log2 * __int_as_float((127 - row_exp[(ld & 1) * 256 + x * 128 + row]) << 23);
-                float c[4] = {sl * ks4.x, sl * ks4.y, sl * ks4.z, sl * ks4.w};
-                const float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w}, inv[4] = {inv4.x, inv4.y, inv4.z, inv4.w};
-                tc::wait_ld();
+                const bool masked = kt < lo || kt + 127 > hi;
+                // Scores of keys 64 hb .. + 63 (two groups); rolled over the halves, and read from tensor
+                // memory once for the maximum and once for the weights, to keep the code small: the
+                // four warps of a scheduler run three different roles, and 1.4 of their 9 cycles per
+                // instruction went to instruction fetches with straight-line code for 128 keys.
+                auto load_half = [&](int hb, float(&v)[2][32]) {
+                    tc::ld_32cols(s_addr + 64 * hb, v[0]);
+                    tc::ld_32cols(s_addr + 64 * hb + 32, v[1]);
+                    tc::wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int g = 0; g < 2; ++g)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const int key = kt + 64 * hb + 32 * g + i;
+                                v[g][i] = key >= lo && key <= hi ? v[g][i] : -INFINITY;
+                            }
+                    }
+                };
+                // c and log2 vs of group 2 hb + g (c positive: -inf x c stays -inf under a scale of 0)
+                auto scales = [&](int hb, int g, float& c, float& lv) {
+                    c = fmaxf(sl * slot[2 * hb + g], 1e-37f);
+                    lv = slot[4 + 2 * hb + g];
+                };
+                auto bias = [&](int hb, int g, float c, float lv, float(&v)[32]) {  // the whole x of a biased score
+                    const float d0 = (float)((int)diag - kt - 64 * hb - 32 * g);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = fmaf(-ab, fabsf(d0 - (float)i), fmaf(v[i], c, lv));
+                };
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int hb = 0; hb < 2; ++hb) {
+                    float v[2][32];
+                    load_half(hb, v);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        float c, lv;
+                        scales(hb, g, c, lv);
+                        if (ALIBI) bias(hb, g, c, lv, v[g]);
+                        float t0 = fmaxf(v[g][0], v[g][1]), t1 = fmaxf(v[g][2], v[g][3]);
+#pragma unroll
+                        for (int i = 4; i < 32; i += 4) {
+                            t0 = max3f(t0, v[g][i], v[g][i + 1]);
+                            t1 = max3f(t1, v[g][i + 2], v[g][i + 3]);
+                        }
+                        t0 = fmaxf(t0, t1);
+                        mx = fmaxf(mx, ALIBI ? t0 : fmaf(t0, c, lv));
+                    }
+                }
+                // S is complete, and so is the P.V before it: their stages are free.  (Told here, not as
+                // soon as S is seen, and not by the issuers' own commits: the copies and the
+                // conversion that follow then fall beside the second pass; 8 % and 15 % faster.)
                 if ((warp & 3) == 0 && lane == 0) {
                     mbar_arrive(&k_empty[(gk + j) % KS]);
                     if (j > 0) mbar_arrive(&vc_empty[(gv + j - 1) & 1]);
-                }
-                if (kt < lo || kt + 127 > hi) {
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        c[g] = fmaxf(c[g], 1e-37f);  // a scale of 0 keeps -inf x c at -inf
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const int key = kt + 32 * g + i;
-                            sv[g][i] = key >= lo && key <= hi ? sv[g][i] : -INFINITY;
-                        }
-                    }
-                }
-                if (ALIBI) {  // the whole x here: c = 1 and log2 vs = 0 below
-                    const float d0 = (float)((int)diag - kt);
-#pragma unroll
-                    for (int g = 0; g < 4; ++g)
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            sv[g][i] = fmaf(-ab, fabsf(d0 - (float)(32 * g + i)), fmaf(sv[g][i], c[g], lv[g]));
-                }
-                float mx = -INFINITY;
-#pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    float t0 = fmaxf(sv[g][0], sv[g][1]), t1 = fmaxf(sv[g][2], sv[g][3]);
-#pragma unroll
-                    for (int i = 4; i < 32; i += 4) {
-                        t0 = max3f(t0, sv[g][i], sv[g][i + 1]);
-                        t1 = max3f(t1, sv[g][i + 2], sv[g][i + 3]);
-                    }
-                    t0 = fmaxf(t0, t1);
-                    mx = fmaxf(mx, ALIBI ? t0 : fmaf(t0, c[g], lv[g]));
                 }
                 const bool grow = mx > m + 8.f;
                 if (__any_sync(0xffffffffu, grow)) {
@@ -613,21 +639,30 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                     }
                 }
                 const float nm = m == -INFINITY ? 0.f : kPqOffset - m;
+#pragma unroll 1
+                for (int hb = 0; hb < 2; ++hb) {
+                    float v[2][32];
+                    load_half(hb, v);
+                    uint32_t pk[32];
 #pragma unroll
-                for (int g = 0; g < 4; ++g) {
-                    const float cg = ALIBI ? 1.f : c[g], ag = ALIBI ? nm : nm + lv[g];
-                    float s0 = 0.f, s1 = 0.f;
-                    uint32_t pk[16];
+                    for (int g = 0; g < 2; ++g) {
+                        float c, lv;
+                        scales(hb, g, c, lv);
+                        if (ALIBI) bias(hb, g, c, lv, v[g]);
+                        const float cg = ALIBI ? 1.f : c, ag = ALIBI ? nm : nm + lv;
+                        float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        float x0, x1;
-                        ffma2(x0, x1, sv[g][2 * i], sv[g][2 * i + 1], cg, cg, ag, ag);
-                        const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                        fadd2_acc(s0, s1, p0, p1);
-                        pk[i] = pack2<__half>(p0, p1);
+                        for (int i = 0; i < 16; ++i) {
+                            float x0, x1;
+                            ffma2(x0, x1, v[g][2 * i], v[g][2 * i + 1], cg, cg, ag, ag);
+                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                            fadd2_acc(s0, s1, p0, p1);
+                            pk[16 * g + i] = pack2<__half>(p0, p1);
+                        }
+                        l = fmaf(s0 + s1, slot[8 + 2 * hb + g], l);
                     }
-                    l = fmaf(s0 + s1, inv[g], l);
-                    tc::st_32x32b_x16(s_addr + 16 * g, pk);
+                    // P of these keys over columns whose S has been read (the first half's)
+                    tc::st_32x32b_x32(s_addr + 32 * hb, pk);
                 }
                 tc::wait_st();
                 tc::fence_before_sync();
