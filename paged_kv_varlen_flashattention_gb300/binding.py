@@ -150,11 +150,27 @@ def describe(t) -> Optional[PaTensor]:
 _PACK = [None] + [struct.Struct(f"Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x").pack_into for n in (1, 2, 3, 4)]
 
 
+_runtime = None  # (torch, current device, raw current stream of a device), bound at the first call
+
+
+def _bind_runtime():
+    global _runtime
+    import torch
+    load()
+    _dtype_codes()
+    current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw_stream is None:
+        raw_stream = lambda index: torch.cuda.current_stream(index).cuda_stream  # noqa: E731
+    _runtime = (torch, current_device, raw_stream)
+    return _runtime
+
+
 def _pack(tensors):
     """(buffer, addresses) of the tensors' descriptors in one buffer that the caller keeps
     alive over the call; None stays None.  About a third of the host time of one ctypes
     structure per tensor."""
-    codes = _dtype_codes()
+    code = _DTYPE_CODES.get
     buf = bytearray(80 * len(tensors))
     at = ctypes.addressof(ctypes.c_char.from_buffer(buf))
     where, off = [], 0
@@ -165,9 +181,9 @@ def _pack(tensors):
             shape = t.shape
             n = len(shape)
             if 1 <= n <= 4:
-                _PACK[n](buf, off, t.data_ptr(), codes.get(t.dtype, -1), n, *shape, *t.stride())
+                _PACK[n](buf, off, t.data_ptr(), code(t.dtype, -1), n, *shape, *t.stride())
             else:  # no rank the library takes: the rank alone, for its refusal
-                _PACK[1](buf, off, t.data_ptr(), codes.get(t.dtype, -1), n, 0, 1)
+                _PACK[1](buf, off, t.data_ptr(), code(t.dtype, -1), n, 0, 1)
             where.append(at + off)
         off += 80
     return buf, where
@@ -176,15 +192,17 @@ def _pack(tensors):
 def _call(fn, on, stream, *args) -> None:
     """fn(*args, stream) with the device of tensor ``on`` current (its current stream when
     ``stream`` is None); raises PaError on a non-zero status."""
-    import torch
+    torch, current_device, raw_stream = _runtime
     index = on.get_device()
-    if index >= 0 and index != torch.cuda.current_device():
+    if index < 0:  # no CUDA tensor: the library refuses it
+        rc = fn(*args, None)
+    elif index == current_device():
+        rc = fn(*args, raw_stream(index) if stream is None else stream.cuda_stream)
+    else:
         with torch.cuda.device(index):
-            return _call(fn, on, stream, *args)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    rc = fn(*args, s.cuda_stream)
+            rc = fn(*args, raw_stream(index) if stream is None else stream.cuda_stream)
     if rc != 0:
-        raise PaError(rc, load().pa_last_error().decode())
+        raise PaError(rc, _lib.pa_last_error().decode())
 
 
 def _ref(d):
@@ -324,13 +342,12 @@ def kv_append_rope(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_ca
     the tokens' positions with the tables ``cos`` / ``sin`` (max_position, rot / 2) fp32,
     and writes k and v into their pages, in place.  Returns the rotated q (``q_out``,
     allocated with torch when not given; pass ``q`` itself to rotate in place) or None."""
-    import torch
-    lib = load()
+    torch = (_runtime or _bind_runtime())[0]
     P = page_block_size if page_block_size is not None else k_cache.shape[1]
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     keep, ds = _pack((q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, q_out))
-    _call(lib.pa_kv_append_rope, k_new, stream, *ds[:5], 1 if interleaved else 0, *ds[5:10], int(P), ds[10])
+    _call(_lib.pa_kv_append_rope, k_new, stream, *ds[:5], 1 if interleaved else 0, *ds[5:10], int(P), ds[10])
     return q_out
 
 
@@ -347,14 +364,13 @@ def kv_append_q8(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_cach
     ``torch.float8_e4m3fn`` codes with the fp32 scales ``k_scale`` / ``v_scale``
     (num_blocks, num_heads_k) of every page and kv head, updated in place.  Without ``cos`` and
     ``sin`` the keys are held as they are (and ``q`` must not be given)."""
-    import torch
-    lib = load()
+    torch = (_runtime or _bind_runtime())[0]
     P = page_block_size if page_block_size is not None else k_cache.shape[1]
     if q is not None and q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     keep, ds = _pack((q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, k_scale,
                       v_scale, q_out))
-    _call(lib.pa_kv_append_q8, k_new, stream, *ds[:5], 1 if interleaved else 0, *ds[5:12], int(P), ds[12])
+    _call(_lib.pa_kv_append_q8, k_new, stream, *ds[:5], 1 if interleaved else 0, *ds[5:12], int(P), ds[12])
     return q_out
 
 
@@ -372,21 +388,21 @@ def varlen_fwd_q8(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlen
     ``torch.float8_e4m3fn`` codes with the fp32 scales ``k_scale`` / ``v_scale`` (num_blocks,
     num_heads_k) of every page and kv head; q and out are f16 or bf16.  Returns (out,
     softmax_lse), allocated with torch when not given."""
-    import torch
-    lib = load()
+    torch = (_runtime or _bind_runtime())[0]
     if max_seqlen_q is None or max_seqlen_k is None:
         raise ValueError("max_seqlen_q and max_seqlen_k are required")
+    shape, device, cache = q.shape, q.device, k_cache.shape
     if softmax_scale is None:
-        softmax_scale = 1.0 / math.sqrt(q.shape[-1])
+        softmax_scale = shape[-1] ** -0.5
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=q.dtype, device=device)
     if softmax_lse is None:
-        softmax_lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
-    P = page_block_size if page_block_size is not None else k_cache.shape[1]
+        softmax_lse = torch.empty((shape[1], shape[0]), dtype=torch.float32, device=device)
     keep, ds = _pack((q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_table, alibi_slopes, out,
                       softmax_lse))
-    _call(lib.pa_varlen_fwd_q8, q, stream, *ds[:8], int(max_seqlen_q), int(max_seqlen_k), q.shape[-2],
-          k_cache.shape[-2], q.shape[-1], int(P), float(softmax_scale), int(window_left), int(window_right), *ds[8:])
+    _call(_lib.pa_varlen_fwd_q8, q, stream, *ds[:8], int(max_seqlen_q), int(max_seqlen_k), shape[-2], cache[-2],
+          shape[-1], int(page_block_size) if page_block_size is not None else cache[1], softmax_scale, window_left,
+          window_right, *ds[8:])
     return out, softmax_lse
 
 

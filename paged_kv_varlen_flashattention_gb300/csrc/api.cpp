@@ -871,7 +871,7 @@ SplitPlan plan_splitkv(const Args& a, bool prefill_takes_long_rows, int prefill_
 SplitPlan plan_q8(const Args& a, bool prefill_takes_long_rows, int prefill_sms, int num_sms) {
     SplitPlan pl{};
     pl.dp = a.D <= 64 ? 64 : a.D <= 128 ? 128 : a.D <= 256 ? 256 : 512;
-    pl.nt = pl.dp == 512 ? 64 : 128;
+    pl.nt = pl.dp >= 256 ? 64 : 128;
     const int G = a.H / a.Hkv;
     const int64_t rows_max = (int64_t)a.max_sq * G;
     pl.rows_cap = prefill_takes_long_rows ? prefill_rows_threshold() : (1 << 30);
@@ -899,7 +899,7 @@ SplitPlan plan_q8(const Args& a, bool prefill_takes_long_rows, int prefill_sms, 
     split_tiles = std::min(split_tiles, std::min<int64_t>(kMaxSplitKeys / pl.nt, tiles_max));
     pl.split_tiles = (int)split_tiles;
     pl.max_splits = (int)std::min<int64_t>((tiles_max + split_tiles - 1) / split_tiles, INT32_MAX);
-    pl.work = pl.row_tiles == 1 && pl.dp <= 256 && a.batch >= kWorkMinBatch && a.batch <= kMaxOrderBatch &&
+    pl.work = pl.row_tiles == 1 && pl.dp <= 128 && a.batch >= kWorkMinBatch && a.batch <= kMaxOrderBatch &&
               pl.max_splits > 1;
     const bool one_wave = units * pl.max_splits <= pl.slots;
     const bool ranked = !pl.work && !one_wave;

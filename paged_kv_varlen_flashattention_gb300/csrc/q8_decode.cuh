@@ -77,7 +77,8 @@ __device__ __forceinline__ uint32_t q8_off(int r, int u) {
         return (uint32_t)((u >> 3) * (NT * 128)) + swz128(r, u & 7);
 }
 
-// Rows' bounds and bias of a tile into shared memory; padding rows attend nothing.
+// Rows' bounds and bias of a tile into shared memory.  Padding rows attend every key: their q is zero,
+// nothing of theirs is written, and so a tile inside the real rows' intervals needs no mask.
 struct Q8Rows {
     int* lo;
     int* hi;
@@ -93,7 +94,7 @@ __device__ __forceinline__ void q8_row_bounds(const SplitParams& p, const TileVi
                                               int M) {
     const int r = threadIdx.x;
     if (r >= M) return;
-    int lo = 0, hi = -1, dg = 0;
+    int lo = 0, hi = INT32_MAX, dg = 0;
     float ab = 0.f;
     if (r < tv.rows) {
         const int64_t i = (tv.row0 + r) / p.G;
@@ -232,9 +233,19 @@ __device__ __forceinline__ void q8_produce(const Q8Params& p, const CUtensorMap*
 __device__ __forceinline__ float q8_score(float s, float c, float lv, bool in, float ab, int dg, int key) {
     return in ? fmaf(-ab, fabsf((float)(dg - key)), fmaf(s, c, lv)) : -INFINITY;
 }
+// Keys [lo, hi] that both of every lane's rows attend and that carry no bias: there a score is one
+// multiply-add (the masks and the bias cost seven instructions a score, a fifth of the kernel).
+__device__ __forceinline__ void q8_plain_keys(bool biased, int& lo, int& hi) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        lo = max(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+        hi = min(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+    }
+    if (biased) hi = -1;
+}
 
 // ---------------------------------------------------------------------------------------------
-// decode_q8_kernel: head_dim <= 256, NW consumer warps with private key slices of every tile
+// decode_q8_kernel: head_dim <= 128, NW consumer warps with private key slices of every tile
 // (as decode_kernel), one producer warp for K and one for V.
 template <int DP_, int MG, int NW, int NT, int STAGES, int ML = MG>
 struct Q8Cfg {
@@ -324,6 +335,8 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
         a[2] = x.y;
         a[3] = y.y;
     };
+    int plain_lo = max(lo0, lo1), plain_hi = min(hi0, hi1);
+    q8_plain_keys(p.alibi != nullptr, plain_lo, plain_hi);
     uint32_t qf[C::Q_IN_REGS ? DP / 16 : 1][4];
     if constexpr (C::Q_IN_REGS) {
 #pragma unroll
@@ -392,8 +405,20 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
                 const int kk0 = key0 + (kb * C::CK + kc) * 16;
                 const int box = (it * NT + kk0) >> p.box_shift;  // a chunk of 16 keys lies in one page
                 const float kss = ksc[box], lv = lvs[box];
-                inv[kc] = exp2f(-lv);
+                inv[kc] = fast_exp2(-lv);
                 const float k0 = c0 * kss, k1 = c1 * kss;
+                if (kt + kk0 >= plain_lo && kt + kk0 + 15 <= plain_hi) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        s[kc][n][0] = fmaf(s[kc][n][0], k0, lv);
+                        s[kc][n][1] = fmaf(s[kc][n][1], k0, lv);
+                        s[kc][n][2] = fmaf(s[kc][n][2], k1, lv);
+                        s[kc][n][3] = fmaf(s[kc][n][3], k1, lv);
+                        mx0 = max3f(mx0, s[kc][n][0], s[kc][n][1]);
+                        mx1 = max3f(mx1, s[kc][n][2], s[kc][n][3]);
+                    }
+                    continue;
+                }
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -584,7 +609,7 @@ __device__ __forceinline__ int q8_sequence(const SplitParams& p, int* rank_len, 
 }
 
 template <typename T, int DP, int MG, int NW, int NT, int STAGES>
-__global__ void __launch_bounds__(NW * 32 + 64, DP <= 128 ? 2 : 1)
+__global__ void __launch_bounds__(NW * 32 + 64, 2)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const Q8Params p) {
     using C = Q8Cfg<DP, MG, NW, NT, STAGES>;
@@ -648,19 +673,21 @@ __global__ void __launch_bounds__(NW * 32 + 64, DP <= 128 ? 2 : 1)
 }
 
 // ---------------------------------------------------------------------------------------------
-// decode512_q8_kernel: head_dim 257..512.
+// decode_q8_wide_kernel: head_dim 129..512.
 //
-// One warp cannot hold 16 rows x 512 columns of O.  Eight warps take key slices of a 64-key tile
+// One warp cannot hold 16 rows x 512 columns of O, and at 256 columns it spills.  Eight warps take key slices of a 64-key tile
 // for Q.K^T (8 keys each of all 16 rows, or 16 keys of one of two row groups), write their
-// weights to shared memory, and after one barrier take 64-column slices for P.V, all keys and
+// weights to shared memory, and after one barrier take DP / 8-column slices for P.V, all keys and
 // both row groups, so V is converted once.  The warps share one reference m per row: a tile whose
 // scores all lie below m + 5 needs no exchange (weights up to 2^15 fit f16); otherwise, a vote
 // folded into that barrier, they exchange row maxima, rescale and write the weights again.  The
 // weights are double-buffered, so the common tile costs one barrier.
-template <int MG>
+template <int DP_, int MG>
 struct Q8WideCfg {
-    static constexpr int DP = 512, NW = 8, NT = 64, M = 16 * MG;
-    static constexpr int KST = 3, VST = MG == 1 ? 3 : 2;
+    static constexpr int DP = DP_, NW = 8, NT = 64, M = 16 * MG;
+    static constexpr int KST = DP == 256 && MG == 2 ? 5 : 3, VST = DP == 256 && MG == 2 ? 5 : DP == 512 && MG == 1 ? 3 : 2;
+    static constexpr int CTAS = DP == 256 && MG == 1 ? 2 : 1;  // an SM
+    static constexpr int UW = DP / 16 / NW;         // 16-column units of a warp's slice
     static constexpr int KS = NW / MG;      // key slices
     static constexpr int NB = NT / KS / 8;  // 8-key tiles per warp
     static constexpr int TILE = NT * DP;
@@ -676,15 +703,15 @@ struct Q8WideCfg {
     static constexpr int OFF_IDS = OFF_SC + 2 * kQ8MaxBoxes * 4;
     static constexpr int SMEM = OFF_IDS + 2 * kQ8MaxBoxes * 4 + 1024;
     static constexpr int THREADS = NW * 32 + 64;
-    static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
+    static_assert(CTAS * (SMEM + 2048) <= 228 * 1024 && SMEM <= 227 * 1024, "shared memory");  // + static and reserved
 };
 
-template <typename T, int MG>
-__global__ void __launch_bounds__(Q8WideCfg<MG>::THREADS, 1)
-    decode512_q8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+template <typename T, int DP_, int MG>
+__global__ void __launch_bounds__(Q8WideCfg<DP_, MG>::THREADS, Q8WideCfg<DP_, MG>::CTAS)
+    decode_q8_wide_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                         const Q8Params p) {
-    using C = Q8WideCfg<MG>;
-    constexpr int DP = C::DP, NT = C::NT, NW = C::NW, M = C::M, NB = C::NB;
+    using C = Q8WideCfg<DP_, MG>;
+    constexpr int DP = C::DP, UW = C::UW, NT = C::NT, NW = C::NW, M = C::M, NB = C::NB;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -751,6 +778,8 @@ __global__ void __launch_bounds__(Q8WideCfg<MG>::THREADS, 1)
     const float c0 = rows.sc[r0], c1 = rows.sc[r1];
     const uint8_t* q0p = smem + C::OFF_Q + r0 * C::QP + tq * 8;
     const uint8_t* q1p = smem + C::OFF_Q + r1 * C::QP + tq * 8;
+    int plain_lo = max(lo0, lo1), plain_hi = min(hi0, hi1);
+    q8_plain_keys(p.alibi != nullptr, plain_lo, plain_hi);
     auto q_frag = [&](int ks, uint32_t (&a)[4]) {
         const uint2 x = *reinterpret_cast<const uint2*>(q0p + ks * 32), y = *reinterpret_cast<const uint2*>(q1p + ks * 32);
         a[0] = x.x;
@@ -758,13 +787,13 @@ __global__ void __launch_bounds__(Q8WideCfg<MG>::THREADS, 1)
         a[2] = x.y;
         a[3] = y.y;
     };
-    float o[MG][8][4];  // [row group][2 x unit + parity]: columns 64 warp + 16 unit + 4 tq + ...
+    float o[MG][2 * UW][4];  // [row group][2 x unit + parity]: columns 16 (UW warp + unit) + 4 tq + ...
     float m[MG][2];     // references of rows 16 g + gq and + 8
 #pragma unroll
     for (int g = 0; g < MG; ++g) {
         m[g][0] = m[g][1] = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < 8; ++n)
+        for (int n = 0; n < 2 * UW; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[g][n][e] = 0.f;
     }
@@ -816,7 +845,9 @@ __global__ void __launch_bounds__(Q8WideCfg<MG>::THREADS, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_empty[kst]);
         const int box = (it * NT + key0) >> p.box_shift;
-        const float kss = ksc[box], lv = lvs[box], inv = exp2f(-lv);
+        const float kss = ksc[box], lv = lvs[box], inv = fast_exp2(-lv);
+        const float k0 = c0 * kss, k1 = c1 * kss;
+        const bool plain = kt + key0 >= plain_lo && kt + key0 + NB * 8 - 1 <= plain_hi;
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -825,13 +856,16 @@ __global__ void __launch_bounds__(Q8WideCfg<MG>::THREADS, 1)
                 const int key = kt + key0 + n * 8 + tq * 2 + (e & 1);
                 float& x = s[0][n][e];
                 x += s[1][n][e];
-                if (e < 2) {
-                    x = q8_score(x, c0 * kss, lv, key >= lo0 && key <= hi0, ab0, dg0, key);
+                if (plain)
+                    x = fmaf(x, e < 2 ? k0 : k1, lv);
+                else if (e < 2)
+                    x = q8_score(x, k0, lv, key >= lo0 && key <= hi0, ab0, dg0, key);
+                else
+                    x = q8_score(x, k1, lv, key >= lo1 && key <= hi1, ab1, dg1, key);
+                if (e < 2)
                     mx0 = fmaxf(mx0, x);
-                } else {
-                    x = q8_score(x, c1 * kss, lv, key >= lo1 && key <= hi1, ab1, dg1, key);
+                else
                     mx1 = fmaxf(mx1, x);
-                }
             }
         uint8_t* ps = smem + C::OFF_P + (it & 1) * (M * 128);
         float sum0, sum1;
@@ -878,7 +912,7 @@ __global__ void __launch_bounds__(Q8WideCfg<MG>::THREADS, 1)
                     m[g][q] = nm;
                 }
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
+                for (int n = 0; n < 2 * UW; ++n) {
                     o[g][n][0] *= f[0];
                     o[g][n][1] *= f[0];
                     o[g][n][2] *= f[1];
@@ -900,10 +934,10 @@ __global__ void __launch_bounds__(Q8WideCfg<MG>::THREADS, 1)
         const bool zeroed = z_lo > 0 || z_hi < NT;
         if (zeroed) {
             uint8_t* vp = smem + C::OFF_V + vst * C::TILE;
-            for (int idx = lane; idx < NT * 4; idx += 32) {
-                const int r = idx >> 2;
+            for (int idx = lane; idx < NT * UW; idx += 32) {
+                const int r = idx / UW;
                 if (r < z_lo || r >= z_hi)
-                    *reinterpret_cast<uint4*>(vp + q8_off<DP, NT>(r, warp * 4 + (idx & 3))) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(vp + q8_off<DP, NT>(r, warp * UW + idx % UW)) = make_uint4(0, 0, 0, 0);
             }
             __syncwarp();
         }
@@ -917,9 +951,9 @@ __global__ void __launch_bounds__(Q8WideCfg<MG>::THREADS, 1)
                     ldsm_x4(p_base + swz128(g * 16 + rr + ((mi & 1) << 3), 2 * ks + (mi >> 1)), a[g][0], a[g][1], a[g][2],
                             a[g][3]);
 #pragma unroll
-                for (int np = 0; np < 2; ++np) {
+                for (int np = 0; np < UW / 2; ++np) {
                     uint32_t v[4];
-                    ldsm_x4_t(v_base + q8_off<DP, NT>(ks * 16 + rr + ((mi & 1) << 3), warp * 4 + 2 * np + (mi >> 1)), v[0],
+                    ldsm_x4_t(v_base + q8_off<DP, NT>(ks * 16 + rr + ((mi & 1) << 3), warp * UW + 2 * np + (mi >> 1)), v[0],
                               v[1], v[2], v[3]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[e] = __byte_perm(v[e], 0, 0x3120);
@@ -966,8 +1000,8 @@ __global__ void __launch_bounds__(Q8WideCfg<MG>::THREADS, 1)
             const int64_t t = tv.q0 + i;
             const int h = hk * p.G + gg;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int d = warp * 64 + u * 16 + tq * 4;
+            for (int u = 0; u < UW; ++u) {
+                const int d = (warp * UW + u) * 16 + tq * 4;
                 if (d >= p.D) continue;
                 const float x0 = o[g][2 * u][2 * q] * iv, x1 = o[g][2 * u + 1][2 * q] * iv;
                 const float x2 = o[g][2 * u][2 * q + 1] * iv, x3 = o[g][2 * u + 1][2 * q + 1] * iv;

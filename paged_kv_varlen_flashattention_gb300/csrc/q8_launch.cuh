@@ -10,7 +10,7 @@
 namespace pa {
 
 // Consumer warps, keys per tile and ring stages per padded head dim: two CTAs an SM with 96 KB of
-// rings each at 64 and 128, one of eight warps with 192 KB at 256.
+// rings each.
 template <int DP>
 struct Q8Shape;
 template <>
@@ -21,10 +21,6 @@ template <>
 struct Q8Shape<128> {
     static constexpr int NW = 4, NT = 128, STAGES = 3;
 };
-template <>
-struct Q8Shape<256> {
-    static constexpr int NW = 8, NT = 128, STAGES = 3;
-};
 
 template <typename T, int DP, int MG>
 struct Q8Kernel {
@@ -34,10 +30,16 @@ struct Q8Kernel {
     static auto kernel() { return decode_q8_kernel<T, DP, MG, S::NW, S::NT, S::STAGES>; }
 };
 template <typename T, int MG>
-struct Q8Kernel<T, 512, MG> {
-    using C = Q8WideCfg<MG>;
+struct Q8Kernel<T, 256, MG> {
+    using C = Q8WideCfg<256, MG>;
     static constexpr int NT = C::NT;
-    static auto kernel() { return decode512_q8_kernel<T, MG>; }
+    static auto kernel() { return decode_q8_wide_kernel<T, 256, MG>; }
+};
+template <typename T, int MG>
+struct Q8Kernel<T, 512, MG> {
+    using C = Q8WideCfg<512, MG>;
+    static constexpr int NT = C::NT;
+    static auto kernel() { return decode_q8_wide_kernel<T, 512, MG>; }
 };
 
 template <typename T, int DP, int MG>
