@@ -899,9 +899,16 @@ SplitPlan plan_q8(const Args& a, bool prefill_takes_long_rows, int prefill_sms, 
     split_tiles = std::min(split_tiles, std::min<int64_t>(kMaxSplitKeys / pl.nt, tiles_max));
     pl.split_tiles = (int)split_tiles;
     pl.max_splits = (int)std::min<int64_t>((tiles_max + split_tiles - 1) / split_tiles, INT32_MAX);
+    pl.cluster = 1;
+    const char* env_cl = std::getenv("PA_Q8_CLUSTER");
+    if (pl.row_tiles == 1 && pl.dp <= 128 && env_cl && !env_tiles) {
+        pl.cluster = std::atoi(env_cl);
+        pl.split_tiles = (int)tiles_max;
+        pl.max_splits = 1;
+    }
     pl.work = pl.row_tiles == 1 && pl.dp <= 128 && a.batch >= kWorkMinBatch && a.batch <= kMaxOrderBatch &&
               pl.max_splits > 1;
-    const bool one_wave = units * pl.max_splits <= pl.slots;
+    const bool one_wave = units * pl.max_splits * pl.cluster <= pl.slots;
     const bool ranked = !pl.work && !one_wave;
     pl.rank_in_cta = ranked && a.batch >= 2 && a.batch <= kRankInCta;
     pl.order_bytes = ranked && a.batch > kRankInCta && a.batch <= kMaxOrderBatch

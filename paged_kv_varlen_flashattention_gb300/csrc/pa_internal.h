@@ -75,6 +75,7 @@ struct SplitPlan {
     int rank_in_cta;     // decode kernel CTAs rank the batch themselves (small batches)
     int tc;              // decode class on the tensor-core decode kernel (128-key tiles)
     int work;            // decode class on the persistent warp-sliced kernel (device work list)
+    int cluster;        // 8-bit cache: CTAs of a cluster that share each unit's keys (then max_splits is 1)
 };
 
 // The decode kernel launches sequences longest first: batches of at most kRankInCta

@@ -39,7 +39,7 @@ struct Q8Params : SplitParams {
     const float* ks;
     const float* vs;
     int64_t ks_s0, ks_s1, vs_s0, vs_s1;
-    int box_shift;  // log2(box_rows)
+    int cluster;    // CTAs of a cluster that share a unit's keys (1: none; splits then go through partials)
 };
 
 constexpr int kQ8MaxBoxes = 256;         // TMA boxes (32 rows or more) of one split
@@ -64,6 +64,70 @@ __device__ __forceinline__ bool q8_wait(uint64_t* bar, uint32_t parity, volatile
 // log2 of a value scale; scales below 2^-100 (zero among them) are read as 2^-100.
 __device__ __forceinline__ float q8_log2_scale(float vs) {
     return vs > 7.8886090522101181e-31f ? fminf(log2f(vs), 126.f) : (float)kScaleExpMin;
+}
+
+// ---- a unit's keys over the CTAs of a cluster --------------------------------------------------
+// Few units (a small batch) or units much longer than the average leave SMs idle or late.  A cluster of
+// 2, 4 or 8 CTAs then takes equal shares of a unit's tiles, leaves each warp's (O, m, l) in its own
+// shared memory, and after a cluster barrier every CTA merges a share of the columns of all of them:
+// no partials in memory and no second launch.  All CTAs of a cluster see the same unit, so they
+// return early together or meet at both barriers; one that gave up says so in its flag, and
+// nobody leaves before the others have read its memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// The part of a warp without a share in the merge: both barriers.
+__device__ __forceinline__ void q8_cluster_passive() {
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+}
+
+// The tiles of a CTA: a fixed count per split, or an equal share of the unit's in a cluster.  False:
+// no work (the same answer in every CTA of a cluster).
+__device__ __forceinline__ bool q8_tiles(const Q8Params& p, const TileView& tv, int split, int& t_begin, int& n_iter,
+                                         bool& single) {
+    if (p.cluster > 1) {
+        t_begin = (int)((int64_t)tv.ntiles * split / p.cluster);
+        n_iter = (int)((int64_t)tv.ntiles * (split + 1) / p.cluster) - t_begin;
+        single = true;
+        return true;
+    }
+    if (split >= max(tv.nsplit, 1)) return false;
+    t_begin = split * p.split_tiles;
+    n_iter = max(0, min(tv.ntiles, t_begin + p.split_tiles) - t_begin);
+    single = tv.nsplit <= 1;
+    return true;
 }
 
 // Byte offset of 16-byte unit `u` of row `r` in a tile of rows of DP bytes as TMA leaves it:
@@ -168,66 +232,95 @@ __device__ __forceinline__ void q8_stage_q(const SplitParams& p, const TileView&
     }
 }
 
-// One producer warp (K or V): the block ids of the split's boxes into `ids`, their scales (as
-// they are, or as log2 for V) into `sc`, the tiles into the ring.  Whole warp; lane 0 issues.
+// One producer warp (K or V): the block ids of the split's boxes into `ids`, the tiles into the
+// ring.  Whole warp; lane 0 issues.  The K producer reports bad block ids.
 template <int DP, int NT, int STAGES>
 __device__ __forceinline__ void q8_produce(const Q8Params& p, const CUtensorMap* map, uint8_t* ring, uint64_t* full,
-                                           uint64_t* empty, uint64_t* sc_full, int* ids, float* sc,
-                                           const float* scales, int64_t s0, int64_t s1, bool as_log2, int b, int hk,
-                                           int sk, int kbeg, int n_iter, int g0, volatile uint32_t* abort_flag) {
+                                           uint64_t* empty, int* ids, bool report, int b, int hk, int sk, int kbeg,
+                                           int n_iter, int g0, volatile uint32_t* abort_flag) {
     constexpr int CB = DP < 128 ? DP : 128, CH = DP / CB;
     const int lane = threadIdx.x & 31;
     const int32_t* bt_row = p.bt + (int64_t)b * p.bt_s0;
     const int n_boxes = min(n_iter * p.boxes_per_tile, kQ8MaxBoxes);
-    float v[kQ8MaxBoxes / 32];
+    // every table entry is requested before the first is looked at: one memory latency
+    int blk[kQ8MaxBoxes / 32];
+#pragma unroll
+    for (int i = 0; i < kQ8MaxBoxes / 32; ++i) {
+        const int bi = lane + 32 * i, key = kbeg + bi * p.box_rows;
+        blk[i] = -1;  // past the sequence: not loaded
+        if (bi < n_boxes && key < sk) {
+            const int page = key / p.P;
+            blk[i] = page < p.bt_cols ? __ldg(bt_row + page) : -2;
+        }
+    }
+    bool bad = false;
 #pragma unroll
     for (int i = 0; i < kQ8MaxBoxes / 32; ++i) {
         const int bi = lane + 32 * i;
-        v[i] = 0.f;
-        if (bi < n_boxes) {
-            const int blk = box_block(bt_row, p.bt_cols, p.num_blocks, p.P, kbeg + bi * p.box_rows, sk, p.err);
-            ids[bi] = blk;
-            if (blk >= 0) v[i] = __ldg(scales + (int64_t)blk * s0 + (int64_t)hk * s1);
+        if (bi >= n_boxes) continue;
+        if (kbeg + bi * p.box_rows < sk && (blk[i] < 0 || blk[i] >= p.num_blocks)) {
+            bad = true;
+            blk[i] = -2;
         }
+        ids[bi] = blk[i];
     }
+    if (bad && report) flag_error(p.err, PA_ERR_DEVICE_BOUNDS);
     __syncwarp();
+    if (lane != 0 || p.withhold) return;
     const uint64_t policy = l2_policy_evict_first();
-    auto issue = [&](int it) -> bool {  // lane 0
+    for (int it = 0; it < n_iter; ++it) {
         const int gi = g0 + it, stage = gi % STAGES;
-        if (gi >= STAGES && !q8_wait(&empty[stage], ((gi / STAGES) - 1) & 1, abort_flag, p.err, p.wait_ns)) return false;
+        if (gi >= STAGES && !q8_wait(&empty[stage], ((gi / STAGES) - 1) & 1, abort_flag, p.err, p.wait_ns)) return;
         uint8_t* st = ring + stage * (NT * DP);
         uint32_t bytes = 0;
         for (int j = 0; j < p.boxes_per_tile; ++j)
             if (ids[it * p.boxes_per_tile + j] >= 0) bytes += (uint32_t)(p.box_rows * DP);
         mbar_arrive_expect_tx(&full[stage], bytes);
         for (int j = 0; j < p.boxes_per_tile; ++j) {
-            const int blk = ids[it * p.boxes_per_tile + j];
-            if (blk < 0) continue;
+            const int box = ids[it * p.boxes_per_tile + j];
+            if (box < 0) continue;
             const int key = kbeg + it * NT + j * p.box_rows;
             const int slot = key - (key / p.P) * p.P;
 #pragma unroll
             for (int c = 0; c < CH; ++c)
-                tma_load_4d(st + c * (NT * CB) + j * p.box_rows * CB, map, &full[stage], c * CB, hk, slot, blk, policy);
+                tma_load_4d(st + c * (NT * CB) + j * p.box_rows * CB, map, &full[stage], c * CB, hk, slot, box, policy);
         }
-        return true;
-    };
-    bool ok = true;
-    int it = 0;
-    if (lane == 0 && !p.withhold)
-        for (; ok && it < min(STAGES, n_iter); ++it) ok = issue(it);
-    // the scales, whose loads ran beside the first copies
-#pragma unroll
-    for (int i = 0; i < kQ8MaxBoxes / 32; ++i) {
-        const int bi = lane + 32 * i;
-        if (bi < n_boxes) sc[bi] = as_log2 ? q8_log2_scale(v[i]) : v[i];
-    }
-    __syncwarp();
-    if (lane == 0) {
-        mbar_arrive(sc_full);
-        if (!p.withhold)
-            for (; ok && it < n_iter; ++it) ok = issue(it);
     }
 }
+
+// The scales of a consumer warp's blocks of keys (each inside one page), K's as it is and V's as
+// log2: lane i holds those of block n & ~31 + i of the warp's sequence of blocks, read straight from
+// the table and the scales beside the producers' copies, 32 blocks ahead of their use.  (Gathered by
+// the producers into shared memory they arrived 4 to 6 us into a unit, after the first copies
+// had been issued; its first keys are there after 3.)
+struct Q8Scales {
+    float ks, lv, ks_next, lv_next;
+    template <typename KeyOf>
+    __device__ __forceinline__ void fetch(const Q8Params& p, int b, int hk, int sk, int n, int n_blocks, KeyOf key_of) {
+        const int i = n + (int)(threadIdx.x & 31);
+        ks_next = 1.f;
+        lv_next = 0.f;
+        if (i >= n_blocks) return;
+        const int key = key_of(i), page = key / p.P;
+        if (key >= sk || page >= p.bt_cols) return;
+        const int blk = __ldg(p.bt + (int64_t)b * p.bt_s0 + page);
+        if (blk < 0 || blk >= p.num_blocks) return;
+        ks_next = __ldg(p.ks + (int64_t)blk * p.ks_s0 + (int64_t)hk * p.ks_s1);
+        lv_next = __ldg(p.vs + (int64_t)blk * p.vs_s0 + (int64_t)hk * p.vs_s1);
+    }
+    // the scales of block n (n goes up by one from call to call; whole warp)
+    template <typename KeyOf>
+    __device__ __forceinline__ void take(const Q8Params& p, int b, int hk, int sk, int n, int n_blocks, KeyOf key_of,
+                                         float& k, float& v) {
+        if ((n & 31) == 0) {
+            ks = ks_next;
+            lv = q8_log2_scale(lv_next);
+            if (n + 32 < n_blocks) fetch(p, b, hk, sk, n + 32, n_blocks, key_of);
+        }
+        k = __shfl_sync(0xffffffffu, ks, n & 31);
+        v = __shfl_sync(0xffffffffu, lv, n & 31);
+    }
+};
 
 // Score of a (row, key): masked by select, biased, in units of V (lv = log2 of its scale).
 __device__ __forceinline__ float q8_score(float s, float c, float lv, bool in, float ab, int dg, int key) {
@@ -253,16 +346,15 @@ struct Q8Cfg {
     static constexpr int M = 16 * MG;
     static constexpr int KW = NW / MG;   // warps sharing a row group
     static constexpr int KPW = NT / KW;  // keys per warp and tile
-    static constexpr int CK = DP <= 128 ? 2 : 1;  // 16-key chunks whose scores are in registers together
+    static constexpr int CK = 2;  // 16-key chunks whose scores are in registers together
     static constexpr int TILE = NT * DP;
     static constexpr int QP = DP * 2 + 32;  // q row pitch: the four rows of a load phase in different banks
     static constexpr int OFF_V = STAGES * TILE;
     static constexpr int OFF_Q = 2 * STAGES * TILE;
     static constexpr int OFF_ROW = OFF_Q + 16 * ML * QP;
-    static constexpr int OFF_BAR = (OFF_ROW + 5 * 16 * ML * 4 + 15) & ~15;  // k_full, k_empty, v_full, v_empty, sc_full
-    static constexpr int OFF_FLAG = OFF_BAR + (4 * STAGES + 1) * 8;
-    static constexpr int OFF_SC = (OFF_FLAG + 4 + 15) & ~15;  // K scales, log2 V scales
-    static constexpr int OFF_IDS = OFF_SC + 2 * kQ8MaxBoxes * 4;
+    static constexpr int OFF_BAR = (OFF_ROW + 5 * 16 * ML * 4 + 15) & ~15;  // k_full, k_empty, v_full, v_empty
+    static constexpr int OFF_FLAG = OFF_BAR + 4 * STAGES * 8;
+    static constexpr int OFF_IDS = (OFF_FLAG + 4 + 15) & ~15;
     static constexpr int SMEM = OFF_IDS + 2 * kQ8MaxBoxes * 4 + 1024;
     static constexpr int THREADS = NW * 32 + 64;
     static constexpr bool Q_IN_REGS = DP <= 128;
@@ -273,11 +365,11 @@ struct Q8Cfg {
     static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 };
 
-// One (sequence, kv head, row tile, split) on a CTA.  Returns whether there was work (uniform):
-// then sc_full went through one phase and the rings through n_done tiles.
+// One (sequence, kv head, row tile, split) on a CTA, whose rings go through n_done tiles.  Returns
+// whether there was work (uniform).
 template <typename T, int DP, int MG, int NW, int NT, int STAGES, int ML>
 __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Q8Params& p,
-                                               uint8_t* smem, int b, int hk, int rt, int split, int g0, int unit,
+                                               uint8_t* smem, int b, int hk, int rt, int split, int g0,
                                                int& n_done) {
     using C = Q8Cfg<DP, MG, NW, NT, STAGES, ML>;
     constexpr int M = C::M;
@@ -285,10 +377,9 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
     TileView tv;
     n_done = 0;
     if (!tile_view<M, NT>(p, b, rt, tv, split == 0)) return false;
-    if (split >= max(tv.nsplit, 1)) return false;
-    const bool single = tv.nsplit <= 1;
-    const int t_begin = split * p.split_tiles;
-    const int n_iter = max(0, min(tv.ntiles, t_begin + p.split_tiles) - t_begin);
+    bool single;
+    int t_begin, n_iter;
+    if (!q8_tiles(p, tv, split, t_begin, n_iter, single)) return false;
     n_done = n_iter;
     const int kbeg = tv.kt0 + t_begin * NT;
 
@@ -297,27 +388,29 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
     uint64_t* k_empty = k_full + STAGES;
     uint64_t* v_full = k_empty + STAGES;
     uint64_t* v_empty = v_full + STAGES;
-    uint64_t* sc_full = v_empty + STAGES;
     volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG);
-    float* ksc = reinterpret_cast<float*>(smem + C::OFF_SC);
-    float* lvs = ksc + kQ8MaxBoxes;
     q8_row_bounds(p, tv, rows, hk, M);
     __syncthreads();  // rows, and for a CTA's first unit the barriers
 
     if (warp >= NW) {
         int* ids = reinterpret_cast<int*>(smem + C::OFF_IDS);
         if (warp == NW)
-            q8_produce<DP, NT, STAGES>(p, &tm_k, smem, k_full, k_empty, sc_full, ids, ksc, p.ks, p.ks_s0, p.ks_s1, false,
-                                       b, hk, tv.sk, kbeg, n_iter, g0, abort_flag);
+            q8_produce<DP, NT, STAGES>(p, &tm_k, smem, k_full, k_empty, ids, true, b, hk, tv.sk, kbeg, n_iter, g0, abort_flag);
         else
-            q8_produce<DP, NT, STAGES>(p, &tm_v, smem + C::OFF_V, v_full, v_empty, sc_full, ids + kQ8MaxBoxes, lvs, p.vs,
-                                       p.vs_s0, p.vs_s1, true, b, hk, tv.sk, kbeg, n_iter, g0, abort_flag);
+            q8_produce<DP, NT, STAGES>(p, &tm_v, smem + C::OFF_V, v_full, v_empty, ids + kQ8MaxBoxes, false, b, hk, tv.sk,
+                                       kbeg, n_iter, g0, abort_flag);
+        if (p.cluster > 1) q8_cluster_passive();
         return true;
     }
+    const int rg = warp / C::KW, kq = warp % C::KW;
+    constexpr int BPT = C::KPW / 32;  // blocks of 32 keys of this warp's slice of a tile
+    static_assert(C::KPW % 32 == 0 && C::CK == 2, "a block is two chunks");
+    auto block_key = [&](int n) { return kbeg + (n / BPT) * NT + kq * C::KPW + (n % BPT) * 32; };
+    Q8Scales scales;
+    scales.fetch(p, b, hk, tv.sk, 0, n_iter * BPT, block_key);
     q8_stage_q<T, DP, M, NW>(p, tv, rows, smem + C::OFF_Q, C::QP, hk, warp, lane);
     named_barrier_sync(1, NW * 32);
 
-    const int rg = warp / C::KW, kq = warp % C::KW;
     const int gq = lane >> 2, tq = lane & 3;
     const int mi = lane >> 3, rr = lane & 7;
     const int r0 = rg * 16 + gq, r1 = r0 + 8;
@@ -348,7 +441,7 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    bool ok = __all_sync(0xffffffffu, q8_wait(sc_full, unit & 1, abort_flag, p.err, p.wait_ns));
+    bool ok = true;
 
     for (int it = 0; ok && it < n_iter; ++it) {
         const int gi = g0 + it, stage = gi % STAGES;
@@ -399,14 +492,12 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
             }
             // scores, row maxima, weights
             float mx0 = -INFINITY, mx1 = -INFINITY;
-            float inv[C::CK];
+            float kss, lv;
+            scales.take(p, b, hk, tv.sk, it * BPT + kb, n_iter * BPT, block_key, kss, lv);
+            const float inv = fast_exp2(-lv), k0 = c0 * kss, k1 = c1 * kss;
 #pragma unroll
             for (int kc = 0; kc < C::CK; ++kc) {
                 const int kk0 = key0 + (kb * C::CK + kc) * 16;
-                const int box = (it * NT + kk0) >> p.box_shift;  // a chunk of 16 keys lies in one page
-                const float kss = ksc[box], lv = lvs[box];
-                inv[kc] = fast_exp2(-lv);
-                const float k0 = c0 * kss, k1 = c1 * kss;
                 if (kt + kk0 >= plain_lo && kt + kk0 + 15 <= plain_hi) {
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
@@ -466,8 +557,8 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
                     w[n][2] = fast_exp2(s[kc][n][2] - u1);
                     w[n][3] = fast_exp2(s[kc][n][3] - u1);
                 }
-                l0 = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), inv[kc], l0);
-                l1 = fmaf((w[0][2] + w[0][3]) + (w[1][2] + w[1][3]), inv[kc], l1);
+                l0 = fmaf((w[0][0] + w[0][1]) + (w[1][0] + w[1][1]), inv, l0);
+                l1 = fmaf((w[0][2] + w[0][3]) + (w[1][2] + w[1][3]), inv, l1);
                 pa[kc][0] = pack2<__half>(w[0][0], w[0][1]);
                 pa[kc][1] = pack2<__half>(w[0][2], w[0][3]);
                 pa[kc][2] = pack2<__half>(w[1][0], w[1][1]);
@@ -517,12 +608,85 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
     l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
     l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-    if (named_barrier_or(1, NW * 32, !ok || *abort_flag != 0u)) return true;  // all leave together
+    const bool gave_up = named_barrier_or(1, NW * 32, !ok || *abort_flag != 0u);
+    if (gave_up && p.cluster <= 1) return true;  // all leave together
     float4* xo = reinterpret_cast<float4*>(smem);  // [warp][n][lane], in the rings
     float4* xml = xo + NW * (DP / 8) * 32;         // [warp][lane]: m0, m1, l0, l1
 #pragma unroll
     for (int n = 0; n < DP / 8; ++n) xo[(warp * (DP / 8) + n) * 32 + lane] = make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
     xml[warp * 32 + lane] = make_float4(m0, m1, l0, l1);
+    T* out = static_cast<T*>(p.out);
+    if (p.cluster > 1) {
+        if (gave_up && tid == 0) *abort_flag = 1u;
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        uint32_t bad = 0;
+        for (int c = 0; c < p.cluster; ++c) bad |= ld_cluster_u32(cluster_addr(const_cast<uint32_t*>(abort_flag), c));
+        if (bad == 0) {
+            // the row group's maxima and sums over the KW slices of every CTA, then this CTA's and warp's
+            // units of its columns
+            const int n_part = p.cluster * C::KW;
+            auto part = [&](int k) { return (rg * C::KW + k % C::KW); };
+            float mm0 = -INFINITY, mm1 = -INFINITY, L0 = 0.f, L1 = 0.f;
+            for (int k = 0; k < n_part; ++k) {
+                const float4 ml = ld_cluster_f4(cluster_addr(&xml[part(k) * 32 + lane], k / C::KW));
+                const float a0 = fmaxf(mm0, ml.x), a1 = fmaxf(mm1, ml.y);
+                const float v0 = a0 == -INFINITY ? 0.f : a0, v1 = a1 == -INFINITY ? 0.f : a1;
+                L0 = L0 * fast_exp2(mm0 - v0) + ml.z * fast_exp2(ml.x - v0);
+                L1 = L1 * fast_exp2(mm1 - v1) + ml.w * fast_exp2(ml.y - v1);
+                mm0 = a0;
+                mm1 = a1;
+            }
+            const float w0 = mm0 == -INFINITY ? 0.f : mm0, w1 = mm1 == -INFINITY ? 0.f : mm1;
+            const float inv0 = L0 == 0.f ? 0.f : 1.f / L0, inv1 = L1 == 0.f ? 0.f : 1.f / L1;
+            for (int u = split * C::KW + kq; u < DP / 16; u += n_part) {
+                float x[2][4] = {};
+                for (int k = 0; k < n_part; ++k) {
+                    const float4 ml = ld_cluster_f4(cluster_addr(&xml[part(k) * 32 + lane], k / C::KW));
+                    const float4 ev = ld_cluster_f4(cluster_addr(&xo[(part(k) * (DP / 8) + 2 * u) * 32 + lane], k / C::KW));
+                    const float4 od = ld_cluster_f4(cluster_addr(&xo[(part(k) * (DP / 8) + 2 * u + 1) * 32 + lane], k / C::KW));
+                    const float e0 = fast_exp2(ml.x - w0) * inv0, e1 = fast_exp2(ml.y - w1) * inv1;
+                    x[0][0] = fmaf(e0, ev.x, x[0][0]);
+                    x[0][1] = fmaf(e0, od.x, x[0][1]);
+                    x[0][2] = fmaf(e0, ev.y, x[0][2]);
+                    x[0][3] = fmaf(e0, od.y, x[0][3]);
+                    x[1][0] = fmaf(e1, ev.z, x[1][0]);
+                    x[1][1] = fmaf(e1, od.z, x[1][1]);
+                    x[1][2] = fmaf(e1, ev.w, x[1][2]);
+                    x[1][3] = fmaf(e1, od.w, x[1][3]);
+                }
+                const int d = u * 16 + tq * 4;
+#pragma unroll
+                for (int hr = 0; hr < 2; ++hr) {
+                    const int row = hr ? r1 : r0;
+                    if (row >= tv.rows || d >= p.D) continue;
+                    const int rho = tv.row0 + row, i = rho / p.G;
+                    const int64_t t = tv.q0 + i;
+                    const int h = hk * p.G + (rho - i * p.G);
+                    *reinterpret_cast<uint2*>(out + t * p.o_s0 + (int64_t)h * p.o_s1 + d) =
+                        make_uint2(pack2<T>(x[hr][0], x[hr][1]), pack2<T>(x[hr][2], x[hr][3]));
+                }
+            }
+            if (split == 0 && kq == 0 && tq == 0) {
+#pragma unroll
+                for (int hr = 0; hr < 2; ++hr) {
+                    const int row = hr ? r1 : r0;
+                    if (row >= tv.rows) continue;
+                    const int rho = tv.row0 + row, i = rho / p.G;
+                    const int64_t t = tv.q0 + i;
+                    const int h = hk * p.G + (rho - i * p.G);
+                    const float L = hr ? L1 : L0, mm = hr ? mm1 : mm0;
+                    p.lse[(int64_t)h * p.lse_s0 + t + (int64_t)b * p.lse_sb] =
+                        L == 0.f ? -INFINITY : (mm - kQ8Offset + log2f(L)) * 0.69314718055994531f;
+                }
+            }
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        return true;
+    }
     named_barrier_sync(1, NW * 32);
     float f0[C::KW], f1[C::KW];
     float L0 = 0.f, L1 = 0.f, mm0 = -INFINITY, mm1 = -INFINITY;
@@ -543,7 +707,6 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
     }
     const float inv0 = L0 == 0.f ? 0.f : 1.f / L0, inv1 = L1 == 0.f ? 0.f : 1.f / L1;
     constexpr int UPW = (DP / 16) / C::KW;  // 16-column units this warp stores
-    T* out = static_cast<T*>(p.out);
 #pragma unroll
     for (int hr = 0; hr < 2; ++hr) {
         const int row = hr ? r1 : r0;
@@ -583,6 +746,373 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
             else
                 p.part_lse[(int64_t)split * p.part_stride + t * p.H + h] = lse;
         }
+    }
+    return true;
+}
+
+// ---------------------------------------------------------------------------------------------
+// The unit above for at most 8 rows (bf16) or 4 (f16), the common decode step: no conversion at all.
+//
+// A 16-row product has room for several e4m3 terms of each row beside one another, so q and the
+// weights are written as sums of terms, t0 + t1 / 16 [+ t2 / 256], each the rounding of what the ones
+// before leave (times 16), term t of row r in row t S + r of the product (S = 8 and two terms, or S = 4
+// and three): one e4m3 product of K or V as they are in the cache takes all terms of a row, and
+// the row's result is the sum over its terms.  Each term takes 4 significant bits and its remainder is
+// at most half its last place: two terms hold a value to 2^-9, three to 2^-13, and the first term's
+// scale (largest q of a row 224..448, largest weight 256) puts the absolute resolution at 2^-14 and
+// 2^-18 of that scale.  Per 32 keys of 128 columns: 32 products and 16 ldmatrix, where the f16
+// form takes 64 products, 16 ldmatrix, 128 conversions and their byte shuffles.  (The e4m3 mma.sync
+// takes 20 cycles of a sub-partition's tensor pipe, two f16 ones of half its depth 17: it is the
+// instructions around them that go.)
+//
+// Each warp takes 32 keys of a 128-key tile.  K rows are read in the order that leaves a lane with the
+// scores of keys 4 t .. 4 t + 3 of each 16, which is how the weights' A fragment wants them.
+template <typename T>
+struct Q8Terms {
+    static constexpr int N = std::is_same<T, __half>::value ? 3 : 2;
+    static constexpr int S = N == 2 ? 8 : 4;  // rows a unit can have
+};
+constexpr float kQ8TermOffset = 8.f;  // largest weight 2^8
+
+template <typename T, int DP, int NW, int NT, int STAGES, int ML>
+__device__ __forceinline__ bool decode_q8_few_rows(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Q8Params& p,
+                                                   uint8_t* smem, int b, int hk, int split, int g0,
+                                                   int& n_done) {
+    using C = Q8Cfg<DP, 1, NW, NT, STAGES, ML>;
+    constexpr int NTERM = Q8Terms<T>::N, S = Q8Terms<T>::S;
+    constexpr int QP = DP + 16;  // q row pitch: eight rows of a fragment load in different banks
+    static_assert(C::KPW == 32, "keys per warp");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    TileView tv;
+    n_done = 0;
+    if (!tile_view<16, NT>(p, b, 0, tv, split == 0)) return false;
+    bool single;
+    int t_begin, n_iter;
+    if (!q8_tiles(p, tv, split, t_begin, n_iter, single)) return false;
+    n_done = n_iter;
+    const int kbeg = tv.kt0 + t_begin * NT;
+
+    const Q8Rows rows = q8_rows(smem + C::OFF_ROW, 16);
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* k_empty = k_full + STAGES;
+    uint64_t* v_full = k_empty + STAGES;
+    uint64_t* v_empty = v_full + STAGES;
+    volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG);
+    q8_row_bounds(p, tv, rows, hk, 16);
+    __syncthreads();  // rows, and for a CTA's first unit the barriers
+
+    if (warp >= NW) {
+        int* ids = reinterpret_cast<int*>(smem + C::OFF_IDS);
+        if (warp == NW)
+            q8_produce<DP, NT, STAGES>(p, &tm_k, smem, k_full, k_empty, ids, true, b, hk, tv.sk, kbeg, n_iter, g0, abort_flag);
+        else
+            q8_produce<DP, NT, STAGES>(p, &tm_v, smem + C::OFF_V, v_full, v_empty, ids + kQ8MaxBoxes, false, b, hk, tv.sk,
+                                       kbeg, n_iter, g0, abort_flag);
+        if (p.cluster > 1) q8_cluster_passive();
+        return true;
+    }
+    auto block_key = [&](int n) { return kbeg + n * NT + warp * 32; };  // 32 aligned keys lie in one page
+    Q8Scales scales;
+    scales.fetch(p, b, hk, tv.sk, 0, n_iter, block_key);
+    // q in its terms, warp w rows w, w + NW, ..., DP / 8 lanes a row; rows without a query are zero
+    uint8_t* qs = smem + C::OFF_Q;
+    {
+        const T* q = static_cast<const T*>(p.q);
+        uint4 x[S / NW];
+#pragma unroll
+        for (int k = 0; k < S / NW; ++k) {
+            const int r = warp + k * NW, i = r / p.G, g = r - i * p.G;
+            x[k] = make_uint4(0, 0, 0, 0);
+            if (r < tv.rows && lane * 8 < p.D)
+                x[k] = __ldg(reinterpret_cast<const uint4*>(q + (int64_t)(tv.q0 + i) * p.q_s0 +
+                                                            (int64_t)(hk * p.G + g) * p.q_s1 + lane * 8));
+        }
+        if (S == 4 && lane * 8 < DP)  // the fourth slot of terms
+            *reinterpret_cast<uint2*>(qs + (12 + warp) * QP + lane * 8) = make_uint2(0, 0);
+#pragma unroll
+        for (int k = 0; k < S / NW; ++k) {
+            const int r = warp + k * NW;
+            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            float v[8], mx = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack2<T>(w[e]);
+                v[2 * e] = f.x;
+                v[2 * e + 1] = f.y;
+                mx = max3f(mx, fabsf(f.x), fabsf(f.y));
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            // the largest power of two with mx 2^e2 <= 448 = 1.75 x 2^8; an infinite element makes the row NaN
+            const int bits = __float_as_int(mx);
+            const int e2 = min(126, 8 - ((bits >> 23) - 127) - ((bits & 0x7fffff) > 0x600000 ? 1 : 0));
+            const float up = mx <= 3.4028235e38f ? __int_as_float((127 + e2) << 23) : NAN;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= up;
+#pragma unroll
+            for (int t = 0; t < NTERM; ++t) {
+                uint32_t c2[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    c2[e] = e4m3x2_take(v[2 * e], v[2 * e + 1]);
+                    v[2 * e] *= 16.f;
+                    v[2 * e + 1] *= 16.f;
+                }
+                if (lane * 8 < DP)
+                    *reinterpret_cast<uint2*>(qs + (t * S + r) * QP + lane * 8) =
+                        make_uint2(c2[0] | (c2[1] << 16), c2[2] | (c2[3] << 16));
+            }
+            if (lane == 0) rows.sc[r] = p.scale_log2 * __int_as_float((127 - e2) << 23);
+        }
+    }
+    named_barrier_sync(1, NW * 32);
+
+    const int gq = lane >> 2, tq = lane & 3;
+    const int mi = lane >> 3, rr = lane & 7;
+    const int row = gq % S;  // with S = 4 lanes of gq and gq + 4 work on the same row
+    const int lo = rows.lo[row], hi = rows.hi[row], dg = rows.dg[row];
+    const float ab = rows.ab[row], cs = rows.sc[row];
+    int plain_lo = lo, plain_hi = hi;
+    q8_plain_keys(p.alibi != nullptr, plain_lo, plain_hi);
+    uint32_t qf[DP / 32][4];
+#pragma unroll
+    for (int ks = 0; ks < DP / 32; ++ks) {
+        const uint8_t* a = qs + gq * QP + ks * 32 + tq * 4;
+        qf[ks][0] = *reinterpret_cast<const uint32_t*>(a);
+        qf[ks][1] = *reinterpret_cast<const uint32_t*>(a + 8 * QP);
+        qf[ks][2] = *reinterpret_cast<const uint32_t*>(a + 16);
+        qf[ks][3] = *reinterpret_cast<const uint32_t*>(a + 8 * QP + 16);
+    }
+    // key of row rr of an 8-key score tile (even or odd) of a 16-key half
+    const int key_of = 4 * (rr >> 1) + (rr & 1);
+    float o[DP / 8][4];
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+
+    const int key0 = warp * 32;
+    for (int it = 0; ok && it < n_iter; ++it) {
+        const int gi = g0 + it, stage = gi % STAGES;
+        const uint32_t par = (gi / STAGES) & 1;
+        const int kt = kbeg + it * NT + key0;  // the warp's first key
+        ok = __all_sync(0xffffffffu, q8_wait(&k_full[stage], par, abort_flag, p.err, p.wait_ns));
+        if (!ok) break;
+        const uint32_t k_base = smem_addr(smem + stage * C::TILE), v_base = smem_addr(smem + C::OFF_V + stage * C::TILE);
+        float kss, lv;
+        scales.take(p, b, hk, tv.sk, it, n_iter, block_key, kss, lv);
+        kss *= cs;
+        float s[4][4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < DP / 32; ++ks)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 16-key halves: their even and odd score tiles
+                uint32_t b0, b1, b2, b3;
+                ldsm_x4(k_base + q8_off<DP, NT>(key0 + 16 * h + key_of + (mi & 2), 2 * ks + (mi & 1)), b0, b1, b2, b3);
+                mma_e4m3(s[2 * h], qf[ks], b0, b1);
+                mma_e4m3(s[2 * h + 1], qf[ks], b2, b3);
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_empty[stage]);
+        // this lane's scores of keys kt + 16 h + 4 tq + {0, 1, 2, 3}
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if constexpr (S == 8) {
+                    x[2 * j + e] = fmaf(s[j][2 + e], 1.f / 16.f, s[j][e]);
+                } else {  // terms 0 and 2 here and term 1 in lane gq ^ 4, or the other way round
+                    const float mine = gq < 4 ? fmaf(s[j][2 + e], 1.f / 256.f, s[j][e]) : s[j][e] * (1.f / 16.f);
+                    x[2 * j + e] = mine + __shfl_xor_sync(0xffffffffu, mine, 16);
+                }
+            }
+        float mx = -INFINITY;
+        if (kt >= plain_lo && kt + 31 <= plain_hi) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], kss, lv);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int key = kt + 16 * (i >> 2) + 4 * tq + (i & 3);
+                x[i] = q8_score(x[i], kss, lv, key >= lo && key <= hi, ab, dg, key);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) mx = max3f(mx, x[i], x[i + 1]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (__any_sync(0xffffffffu, mx > m)) {
+            const float nm = fmaxf(m, mx);
+            const float f = nm == -INFINITY ? 1.f : fast_exp2(m - nm);
+            m = nm;
+            l *= f;
+            // rows gq and gq + 8 of the product hold terms of the same row
+#pragma unroll
+            for (int n = 0; n < DP / 8; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][e] *= f;
+        }
+        const float u = m == -INFINITY ? 0.f : m - kQ8TermOffset;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            x[i] = fast_exp2(x[i] - u);
+            sum += x[i];
+        }
+        l = fmaf(sum, fast_exp2(-lv), l);
+        // the weights' terms: A rows gq (columns 4 tq .. + 3 of either half) and gq + 8
+        uint32_t pa[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float* w = &x[4 * h];
+            uint32_t t[3];
+#pragma unroll
+            for (int k = 0; k < NTERM; ++k) {
+                const uint32_t c0 = e4m3x2_take(w[0], w[1]), c1 = e4m3x2_take(w[2], w[3]);
+                t[k] = c0 | (c1 << 16);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] *= 16.f;
+            }
+            if constexpr (S == 8) {
+                pa[2 * h] = t[0];
+                pa[2 * h + 1] = t[1];
+            } else {
+                pa[2 * h] = gq < 4 ? t[0] : t[1];
+                pa[2 * h + 1] = gq < 4 ? t[2] : 0u;
+            }
+        }
+        ok = __all_sync(0xffffffffu, q8_wait(&v_full[stage], par, abort_flag, p.err, p.wait_ns));
+        if (!ok) break;
+        // V rows of this warp's keys that no row attends become 0 (0 x NaN is NaN): keys before the first
+        // interval, past the last, and slots that were never loaded
+        const bool zeroed = kt < tv.lo || kt + 31 > tv.hi;
+        if (zeroed) {
+            if (kt + lane < tv.lo || kt + lane > tv.hi) {
+                uint8_t* vst = smem + C::OFF_V + stage * C::TILE;
+#pragma unroll
+                for (int un = 0; un < DP / 16; ++un)
+                    *reinterpret_cast<uint4*>(vst + q8_off<DP, NT>(key0 + lane, un)) = make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int un = 0; un < DP / 16; ++un) {
+            uint32_t v0, v1, v2, v3;
+            ldsm_b8_x2_t(v_base + q8_off<DP, NT>(key0 + lane, un), v0, v1, v2, v3);
+            mma_e4m3(o[2 * un], pa, v0, v2);
+            mma_e4m3(o[2 * un + 1], pa, v1, v3);
+        }
+        if (zeroed) fence_proxy_async_smem();  // the stage is rewritten by TMA later
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&v_empty[stage]);
+    }
+
+    // ---- sum the terms, then merge the key slices of the warps, each a share of the columns ----
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    const bool gave_up = named_barrier_or(1, NW * 32, !ok || *abort_flag != 0u);
+    if (gave_up && p.cluster <= 1) return true;  // all leave together
+    float2* xo = reinterpret_cast<float2*>(smem);  // [warp][n][lane], in the rings
+    float2* xml = xo + NW * (DP / 8) * 32;         // [warp][lane]: m, l
+#pragma unroll
+    for (int n = 0; n < DP / 8; ++n) {
+        float2 v;
+        if constexpr (S == 8) {
+            v = make_float2(fmaf(o[n][2], 1.f / 16.f, o[n][0]), fmaf(o[n][3], 1.f / 16.f, o[n][1]));
+        } else {
+            v = gq < 4 ? make_float2(fmaf(o[n][2], 1.f / 256.f, o[n][0]), fmaf(o[n][3], 1.f / 256.f, o[n][1]))
+                       : make_float2(o[n][0] * (1.f / 16.f), o[n][1] * (1.f / 16.f));
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
+        }
+        xo[(warp * (DP / 8) + n) * 32 + lane] = v;
+    }
+    xml[warp * 32 + lane] = make_float2(m, l);
+    const int oi = row / p.G, oh = hk * p.G + (row - oi * p.G);  // the row's query and head
+    T* orow = static_cast<T*>(p.out) + ((int64_t)tv.q0 + oi) * p.o_s0 + (int64_t)oh * p.o_s1;
+    const bool mine = gq < S && gq < tv.rows;
+    if (p.cluster > 1) {
+        if (gave_up && tid == 0) *abort_flag = 1u;
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        uint32_t bad = 0;
+        for (int c = 0; c < p.cluster; ++c) bad |= ld_cluster_u32(cluster_addr(const_cast<uint32_t*>(abort_flag), c));
+        if (bad == 0 && mine) {
+            const int n_part = p.cluster * NW;
+            float mm = -INFINITY, L = 0.f;
+            for (int k = 0; k < n_part; ++k) {
+                const float2 ml = ld_cluster_f2(cluster_addr(&xml[(k % NW) * 32 + lane], k / NW));
+                const float a = fmaxf(mm, ml.x), v = a == -INFINITY ? 0.f : a;
+                L = L * fast_exp2(mm - v) + ml.y * fast_exp2(ml.x - v);
+                mm = a;
+            }
+            const float um = mm == -INFINITY ? 0.f : mm, iv = L == 0.f ? 0.f : 1.f / L;
+            for (int n = split * NW + warp; n < DP / 8; n += n_part) {
+                float x0 = 0.f, x1 = 0.f;
+                for (int k = 0; k < n_part; ++k) {
+                    const float2 ml = ld_cluster_f2(cluster_addr(&xml[(k % NW) * 32 + lane], k / NW));
+                    const float2 v = ld_cluster_f2(cluster_addr(&xo[((k % NW) * (DP / 8) + n) * 32 + lane], k / NW));
+                    const float e = fast_exp2(ml.x - um) * iv;
+                    x0 = fmaf(e, v.x, x0);
+                    x1 = fmaf(e, v.y, x1);
+                }
+                const int d = n * 8 + tq * 2;
+                if (d < p.D) *reinterpret_cast<uint32_t*>(orow + d) = pack2<T>(x0, x1);
+            }
+            if (split == 0 && warp == 0 && tq == 0)
+                p.lse[(int64_t)oh * p.lse_s0 + tv.q0 + oi + (int64_t)b * p.lse_sb] =
+                    L == 0.f ? -INFINITY : (mm - kQ8TermOffset + log2f(L)) * 0.69314718055994531f;
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        return true;
+    }
+    named_barrier_sync(1, NW * 32);
+    float f[NW], L = 0.f, mm = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) mm = fmaxf(mm, xml[k * 32 + lane].x);
+    const float um = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+    for (int k = 0; k < NW; ++k) {
+        const float2 ml = xml[k * 32 + lane];
+        f[k] = fast_exp2(ml.x - um);
+        L += f[k] * ml.y;
+    }
+    if (!mine) return true;
+    const float iv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t t = tv.q0 + oi;
+#pragma unroll
+    for (int nn = 0; nn < (DP / 8) / NW; ++nn) {
+        const int n = warp * ((DP / 8) / NW) + nn, d = n * 8 + tq * 2;
+        if (d >= p.D) continue;
+        float x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            const float2 v = xo[(k * (DP / 8) + n) * 32 + lane];
+            x0 = fmaf(f[k], v.x, x0);
+            x1 = fmaf(f[k], v.y, x1);
+        }
+        if (single)
+            *reinterpret_cast<uint32_t*>(orow + d) = pack2<T>(x0 * iv, x1 * iv);
+        else
+            *reinterpret_cast<float2*>(p.part_o + ((int64_t)split * p.part_stride + t * p.H + oh) * p.D + d) =
+                make_float2(x0 * iv, x1 * iv);
+    }
+    if (warp == 0 && tq == 0) {
+        const float lse = L == 0.f ? -INFINITY : (mm - kQ8TermOffset + log2f(L)) * 0.69314718055994531f;
+        if (single)
+            p.lse[(int64_t)oh * p.lse_s0 + t + (int64_t)b * p.lse_sb] = lse;
+        else
+            p.part_lse[(int64_t)split * p.part_stride + t * p.H + oh] = lse;
     }
     return true;
 }
@@ -628,26 +1158,28 @@ __global__ void __launch_bounds__(NW * 32 + 64, 2)
             mbar_init(&bars[2 * STAGES + s], 1);   // v_full
             mbar_init(&bars[3 * STAGES + s], NW);  // v_empty
         }
-        mbar_init(&bars[4 * STAGES], 2);
         *abort_flag = 0u;
         fence_mbar_init();
     }
-    // A kernel for two row groups runs a sequence of at most 16 rows on the one-group body.
-    auto run_unit = [&](int b, int hk, int rt, int split, int g0, int unit, int& n_done) -> bool {
+    // A sequence of few rows runs on the body for them, and in a kernel for two row groups one of at
+    // most 16 rows on the one-group body.
+    auto run_unit = [&](int b, int hk, int rt, int split, int g0, int& n_done) -> bool {
+        if (rt == 0 && b >= 0 && b < p.batch && (int64_t)(p.cu_q[b + 1] - p.cu_q[b]) * p.G <= Q8Terms<T>::S)
+            return decode_q8_few_rows<T, DP, NW, NT, STAGES, MG>(tm_k, tm_v, p, smem, b, hk, split, g0, n_done);
         if constexpr (MG == 2) {
             using L1 = Q8Cfg<DP, 1, NW, NT, STAGES, 2>;
-            static_assert(L1::OFF_ROW == C::OFF_ROW && L1::OFF_BAR == C::OFF_BAR && L1::OFF_SC == C::OFF_SC &&
+            static_assert(L1::OFF_ROW == C::OFF_ROW && L1::OFF_BAR == C::OFF_BAR && L1::OFF_IDS == C::OFF_IDS &&
                               L1::SMEM == C::SMEM,
                           "both bodies share one shared-memory layout");
             if (b >= 0 && b < p.batch && (int64_t)(p.cu_q[b + 1] - p.cu_q[b]) * p.G <= 16)
-                return decode_q8_unit<T, DP, 1, NW, NT, STAGES, 2>(tm_k, tm_v, p, smem, b, hk, rt, split, g0, unit, n_done);
+                return decode_q8_unit<T, DP, 1, NW, NT, STAGES, 2>(tm_k, tm_v, p, smem, b, hk, rt, split, g0, n_done);
         }
-        return decode_q8_unit<T, DP, MG, NW, NT, STAGES, MG>(tm_k, tm_v, p, smem, b, hk, rt, split, g0, unit, n_done);
+        return decode_q8_unit<T, DP, MG, NW, NT, STAGES, MG>(tm_k, tm_v, p, smem, b, hk, rt, split, g0, n_done);
     };
     if (p.work) {  // persistent: (sequence, split) x kv head items in list order
         __shared__ int s_item;
         const int total = p.work[1] * p.Hkv;
-        int g0 = 0, unit = 0;
+        int g0 = 0;
         for (;;) {
             if (tid == 0) s_item = atomicAdd(p.work, 1);
             __syncthreads();
@@ -655,12 +1187,11 @@ __global__ void __launch_bounds__(NW * 32 + 64, 2)
             if (w >= total) break;
             const int pair = w / p.Hkv;
             int n_done = 0;
-            const bool ran = run_unit(p.work[2 + 2 * pair], w - pair * p.Hkv, 0, p.work[3 + 2 * pair], g0, unit, n_done);
+            run_unit(p.work[2 + 2 * pair], w - pair * p.Hkv, 0, p.work[3 + 2 * pair], g0, n_done);
             fence_proxy_async_smem();  // the merge's writes come before the next item's copies
             __syncthreads();
             if (*abort_flag) break;
             g0 += n_done;
-            unit += ran ? 1 : 0;
         }
         return;
     }
@@ -669,7 +1200,7 @@ __global__ void __launch_bounds__(NW * 32 + 64, 2)
     const int b = q8_sequence(p, rank_len, &rank_pick);
     if (tid >= NW * 32 && tid < NW * 32 + 32) prefetch_split_pages<NT>(p, b, (int)blockIdx.x, tid - NW * 32);
     int n_done = 0;
-    run_unit(b, (int)blockIdx.y % p.Hkv, (int)blockIdx.y / p.Hkv, (int)blockIdx.x, 0, 0, n_done);
+    run_unit(b, (int)blockIdx.y % p.Hkv, (int)blockIdx.y / p.Hkv, (int)blockIdx.x, 0, n_done);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -698,9 +1229,8 @@ struct Q8WideCfg {
     static constexpr int OFF_ROW = OFF_Q + M * QP;
     static constexpr int OFF_MAX = OFF_ROW + 5 * M * 4;      // [key slice][row]: maxima, then sums
     static constexpr int OFF_BAR = (OFF_MAX + KS * M * 4 + 15) & ~15;
-    static constexpr int OFF_FLAG = OFF_BAR + (2 * KST + 2 * VST + 1) * 8;
-    static constexpr int OFF_SC = (OFF_FLAG + 4 + 15) & ~15;
-    static constexpr int OFF_IDS = OFF_SC + 2 * kQ8MaxBoxes * 4;
+    static constexpr int OFF_FLAG = OFF_BAR + (2 * KST + 2 * VST) * 8;
+    static constexpr int OFF_IDS = (OFF_FLAG + 4 + 15) & ~15;
     static constexpr int SMEM = OFF_IDS + 2 * kQ8MaxBoxes * 4 + 1024;
     static constexpr int THREADS = NW * 32 + 64;
     static_assert(CTAS * (SMEM + 2048) <= 228 * 1024 && SMEM <= 227 * 1024, "shared memory");  // + static and reserved
@@ -722,7 +1252,6 @@ __global__ void __launch_bounds__(Q8WideCfg<DP_, MG>::THREADS, Q8WideCfg<DP_, MG
     uint64_t* k_empty = k_full + C::KST;
     uint64_t* v_full = k_empty + C::KST;
     uint64_t* v_empty = v_full + C::VST;
-    uint64_t* sc_full = v_empty + C::VST;
     volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG);
     if (tid == 0) {
         for (int s = 0; s < C::KST; ++s) {
@@ -733,7 +1262,6 @@ __global__ void __launch_bounds__(Q8WideCfg<DP_, MG>::THREADS, Q8WideCfg<DP_, MG
             mbar_init(&v_full[s], 1);
             mbar_init(&v_empty[s], NW);
         }
-        mbar_init(sc_full, 2);
         *abort_flag = 0u;
         fence_mbar_init();
     }
@@ -749,25 +1277,25 @@ __global__ void __launch_bounds__(Q8WideCfg<DP_, MG>::THREADS, Q8WideCfg<DP_, MG
     const int n_iter = max(0, min(tv.ntiles, t_begin + p.split_tiles) - t_begin);
     const int kbeg = tv.kt0 + t_begin * NT;
     const Q8Rows rows = q8_rows(smem + C::OFF_ROW, M);
-    float* ksc = reinterpret_cast<float*>(smem + C::OFF_SC);
-    float* lvs = ksc + kQ8MaxBoxes;
     float* xmax = reinterpret_cast<float*>(smem + C::OFF_MAX);
     q8_row_bounds(p, tv, rows, hk, M);
     __syncthreads();
     if (warp >= NW) {
         int* ids = reinterpret_cast<int*>(smem + C::OFF_IDS);
         if (warp == NW)
-            q8_produce<DP, NT, C::KST>(p, &tm_k, smem, k_full, k_empty, sc_full, ids, ksc, p.ks, p.ks_s0, p.ks_s1, false,
-                                       b, hk, tv.sk, kbeg, n_iter, 0, abort_flag);
+            q8_produce<DP, NT, C::KST>(p, &tm_k, smem, k_full, k_empty, ids, true, b, hk, tv.sk, kbeg, n_iter, 0, abort_flag);
         else
-            q8_produce<DP, NT, C::VST>(p, &tm_v, smem + C::OFF_V, v_full, v_empty, sc_full, ids + kQ8MaxBoxes, lvs, p.vs,
-                                       p.vs_s0, p.vs_s1, true, b, hk, tv.sk, kbeg, n_iter, 0, abort_flag);
+            q8_produce<DP, NT, C::VST>(p, &tm_v, smem + C::OFF_V, v_full, v_empty, ids + kQ8MaxBoxes, false, b, hk, tv.sk,
+                                       kbeg, n_iter, 0, abort_flag);
         return;
     }
+    const int rg = warp / C::KS, slice = warp % C::KS;
+    auto block_key = [&](int n) { return kbeg + n * NT + slice * NB * 8; };
+    Q8Scales scales;
+    scales.fetch(p, b, hk, tv.sk, 0, n_iter, block_key);
     q8_stage_q<T, DP, M, NW>(p, tv, rows, smem + C::OFF_Q, C::QP, hk, warp, lane);
     named_barrier_sync(1, NW * 32);
 
-    const int rg = warp / C::KS, slice = warp % C::KS;
     const int gq = lane >> 2, tq = lane & 3;
     const int mi = lane >> 3, rr = lane & 7;
     const int r0 = rg * 16 + gq, r1 = r0 + 8;  // this warp's rows in Q.K^T
@@ -799,7 +1327,7 @@ __global__ void __launch_bounds__(Q8WideCfg<DP_, MG>::THREADS, Q8WideCfg<DP_, MG
     }
     auto mine = [&](int q) { return MG == 2 && rg ? m[MG - 1][q] : m[0][q]; };  // of this warp's Q.K^T rows
     float l0 = 0.f, l1 = 0.f;  // sums of this warp's rows over its keys
-    bool ok = __all_sync(0xffffffffu, q8_wait(sc_full, 0, abort_flag, p.err, p.wait_ns));
+    bool ok = true;
 
     for (int it = 0; it < n_iter; ++it) {
         const int kst = it % C::KST, vst = it % C::VST;
@@ -844,10 +1372,11 @@ __global__ void __launch_bounds__(Q8WideCfg<DP_, MG>::THREADS, Q8WideCfg<DP_, MG
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&k_empty[kst]);
-        const int box = (it * NT + key0) >> p.box_shift;
-        const float kss = ksc[box], lv = lvs[box], inv = fast_exp2(-lv);
+        float kss, lv;
+        scales.take(p, b, hk, tv.sk, it, n_iter, block_key, kss, lv);
+        const float inv = fast_exp2(-lv);
         const float k0 = c0 * kss, k1 = c1 * kss;
-        const bool plain = kt + key0 >= plain_lo && kt + key0 + NB * 8 - 1 <= plain_hi;
+        const bool plain = MG == 1 && kt + key0 >= plain_lo && kt + key0 + NB * 8 - 1 <= plain_hi;  // (two groups: spills)
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int n = 0; n < NB; ++n)

@@ -80,8 +80,26 @@ static int run_q8(const CUtensorMap& tk, const CUtensorMap& tv, const Q8Params& 
     {
         NvtxRange nv("pa::decode_q8_kernel");
         timer_begin(PA_KC_SPLITKV, stream);
-        K::kernel()<<<grid, K::C::THREADS, K::C::SMEM, stream>>>(tk, tv, sp);
-        if ((e = cudaGetLastError()) != cudaSuccess) {
+        if (sp.cluster > 1) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(sp.cluster, sp.Hkv, sp.batch);
+            cfg.blockDim = dim3(K::C::THREADS);
+            cfg.dynamicSmemBytes = K::C::SMEM;
+            cfg.stream = stream;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = sp.cluster;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, K::kernel(), tk, tv, sp);
+            if (e == cudaSuccess) e = cudaGetLastError();
+        } else {
+            K::kernel()<<<grid, K::C::THREADS, K::C::SMEM, stream>>>(tk, tv, sp);
+            e = cudaGetLastError();
+        }
+        if (e != cudaSuccess) {
             snprintf(msg, msg_len, "q8 decode launch: %s", cudaGetErrorString(e));
             return PA_ERR_CUDA;
         }
@@ -156,7 +174,6 @@ static int launch_q8_t(const Args& a, const SplitPlan& plan, void* workspace, un
     sp.paged = 1;
     sp.box_rows = box_rows;
     sp.boxes_per_tile = NT / box_rows;
-    sp.box_shift = box_rows == 128 ? 7 : box_rows == 64 ? 6 : 5;
     sp.max_sq = a.max_sq;
     sp.max_sk = a.max_sk;
     sp.scale_log2 = a.scale * 1.4426950408889634f;
@@ -178,6 +195,7 @@ static int launch_q8_t(const Args& a, const SplitPlan& plan, void* workspace, un
     sp.err = err;
     sp.wait_ns = a.wait_ns;
     sp.withhold = a.withhold_loads;
+    sp.cluster = plan.cluster;
     sp.ks = a.k_scale;
     sp.vs = a.v_scale;
     sp.ks_s0 = a.ks_s0;

@@ -3,10 +3,15 @@
 
 Tolerance.  The codes are exact in f16 and the products accumulate in fp32, so a score s (log2
 units, |s| <= 64 here) is off by at most 2^-16 for inputs of a few units: 2^-16 ln 2 relative on a
-weight.  The weights are rounded to f16 for the product with V: at most 2^-11 each, relative.  With
-A = sum_j p_j |V_j| the output before its own rounding is then off by at most (2^-11 + 2^-15) A, and
-the rounding to the type adds eps / 2 of the value (2^-8 bf16, 2^-11 f16) and half a subnormal
-step.  lse is off by at most 2^-16 from the scores plus fp32 roundings: 2e-5."""
+weight.  The weights are rounded for the product with V, at most w each, relative: to f16, w = 2^-11;
+in bf16 calls of few rows to two e4m3 terms, of which the first leaves at most half its last place
+(2^-4 of the power of two at the weight) and the second half its own (2^-5 of the power of two below
+that): w = 2^-9; f16 calls of few rows take three terms, within 2^-11.  A weight below the terms' range
+is off by at most half of 2^-13 on the scale where the row's largest weight is 2^8: 2^-22 of the
+largest, and the weights sum to at least the largest.  With A = sum_j p_j |V_j| the output before its
+own rounding is then off by at most (w + 2^-15) A + 2^-22 sum_j |V_j| over the row's keys, and the
+rounding to the type adds eps / 2 of the value (2^-8 bf16, 2^-11 f16) and half a subnormal step.
+lse is off by at most 2^-16 from the scores plus fp32 roundings: 2e-5."""
 import pytest
 import torch
 
@@ -54,7 +59,12 @@ def check(x, out, lse, wl=-1, wr=0, scale=None, slopes=None, wide_rows=False):
     ref, ref_l = _q8.attention(x["q"], kk, vv, *args)
     mag, _ = _q8.attention(x["q"], kk, vv.abs(), *args)
     t = _q8.TORCH[x["dtype"]]
-    tol = (2.0 ** -11 + 2.0 ** -15) * mag + torch.finfo(t).eps / 2 * ref.abs() * (1 + 2 ** -8) + \
+    w = 2.0 ** -9 if x["dtype"] == "bf16" else 2.0 ** -11
+    seq = torch.repeat_interleave(torch.arange(len(x["sq"])), torch.tensor(x["sq"], dtype=torch.long))
+    below = torch.stack([vv[x["bt"][b, :(m + vv.shape[1] - 1) // vv.shape[1]].long()].abs().sum((0, 1)) if m else
+                         torch.zeros(vv.shape[2:], dtype=torch.float64) for b, m in enumerate(x["sk"])])
+    below = below[seq].repeat_interleave(x["q"].shape[1] // vv.shape[2], 1)  # sum |V| of a row's sequence
+    tol = (w + 2.0 ** -15) * mag + 2.0 ** -22 * below + torch.finfo(t).eps / 2 * ref.abs() * (1 + 2 ** -8) + \
         torch.finfo(t).smallest_normal * torch.finfo(t).eps / 2
     lse_tol = 2e-5 + 1e-6 * ref_l.abs()
     if wide_rows:
