@@ -24,7 +24,6 @@
 namespace pa {
 namespace {
 
-constexpr int kQ8Threads = 128;
 constexpr int kQ8Held = 2;   // units of K and of V a thread keeps in registers
 constexpr int kQ8QPasses = 4;  // passes of q heads per warp
 
@@ -51,9 +50,10 @@ __device__ __forceinline__ float finite_absmax16(const float (&x)[16]) {
 }
 
 // Earlier tokens of a page (slots 0 .. kept - 1 of one head) held again under a larger scale.
+template <int NT>
 __device__ __forceinline__ void rescale_slots(uint8_t* row0, int64_t slot_stride, int kept, int D, float ratio) {
     const int units = D / 16;
-    for (int i = threadIdx.x; i < kept * units; i += kQ8Threads) {
+    for (int i = threadIdx.x; i < kept * units; i += NT) {
         uint4* p = reinterpret_cast<uint4*>(row0 + (int64_t)(i / units) * slot_stride + (i % units) * 16);
         uint4 v = *p;
         uint32_t* w = reinterpret_cast<uint32_t*>(&v);
@@ -67,8 +67,8 @@ __device__ __forceinline__ void rescale_slots(uint8_t* row0, int64_t slot_stride
     }
 }
 
-template <typename T, bool INTERLEAVED>
-__global__ void __launch_bounds__(kQ8Threads)
+template <typename T, bool INTERLEAVED, int NT>
+__global__ void __launch_bounds__(NT)
     q8_append_kernel(const RopeArgs a, int64_t page_ctas, int passes, int items_per_token, int64_t q_items,
                      unsigned int* err) {
     const AppendArgs& k = a.kv;
@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kQ8Threads)
     const int units = k.D / 16;
     if (blockIdx.x >= page_ctas) {
         // ---- q: one (token, few heads) item a warp ----
-        const int64_t item = ((int64_t)blockIdx.x - page_ctas) * (kQ8Threads / 32) + warp;
+        const int64_t item = ((int64_t)blockIdx.x - page_ctas) * (NT / 32) + warp;
         if (item >= q_items) return;
         const int64_t t = item / items_per_token;
         const int pass0 = (int)(item - t * items_per_token) * kQ8QPasses;
@@ -176,13 +176,13 @@ __global__ void __launch_bounds__(kQ8Threads)
             rotate16<INTERLEAVED>(xk, c, s);
         }
     };
-    const bool held = n_units <= kQ8Threads * kQ8Held;
+    const bool held = n_units <= NT * kQ8Held;
     float hk_[kQ8Held][16], hv_[kQ8Held][16];
     float mk = 0.f, mv = 0.f;
     if (held) {
 #pragma unroll
         for (int r = 0; r < kQ8Held; ++r) {
-            const int i = tid + r * kQ8Threads;
+            const int i = tid + r * NT;
             if (i < n_units) {
                 fetch(i, hk_[r], hv_[r]);
                 mk = fmaxf(mk, finite_absmax16(hk_[r]));
@@ -190,14 +190,14 @@ __global__ void __launch_bounds__(kQ8Threads)
             }
         }
     } else {
-        for (int i = tid; i < n_units; i += kQ8Threads) {
+        for (int i = tid; i < n_units; i += NT) {
             float xk[16], xv[16];
             fetch(i, xk, xv);
             mk = fmaxf(mk, finite_absmax16(xk));
             mv = fmaxf(mv, finite_absmax16(xv));
         }
     }
-    __shared__ float red[2][kQ8Threads / 32];
+    __shared__ float red[2][NT / 32];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
@@ -209,14 +209,14 @@ __global__ void __launch_bounds__(kQ8Threads)
     }
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kQ8Threads / 32; ++w) {
+    for (int w = 0; w < NT / 32; ++w) {
         mk = fmaxf(mk, red[0][w]);
         mv = fmaxf(mv, red[1][w]);
     }
     const float new_k = fmaxf(old_k, pow2_scale(mk)), new_v = fmaxf(old_v, pow2_scale(mv));
     if (s_lo > 0) {
-        if (new_k > old_k) rescale_slots(kc, k.c_s1, s_lo, k.D, old_k / new_k);
-        if (new_v > old_v) rescale_slots(vc, k.c_s1, s_lo, k.D, old_v / new_v);
+        if (new_k > old_k) rescale_slots<NT>(kc, k.c_s1, s_lo, k.D, old_k / new_k);
+        if (new_v > old_v) rescale_slots<NT>(vc, k.c_s1, s_lo, k.D, old_v / new_v);
     }
     if (tid == 0) {
         *ks = new_k;
@@ -237,16 +237,25 @@ __global__ void __launch_bounds__(kQ8Threads)
     if (held) {
 #pragma unroll
         for (int r = 0; r < kQ8Held; ++r) {
-            const int i = tid + r * kQ8Threads;
+            const int i = tid + r * NT;
             if (i < n_units) put(i, hk_[r], hv_[r]);
         }
     } else {
-        for (int i = tid; i < n_units; i += kQ8Threads) {
+        for (int i = tid; i < n_units; i += NT) {
             float xk[16], xv[16];
             fetch(i, xk, xv);
             put(i, xk, xv);
         }
     }
+}
+
+using Q8AppendKernel = void (*)(const RopeArgs, int64_t, int, int, int64_t, unsigned int*);
+
+template <typename T>
+Q8AppendKernel q8_append_kernel_of(bool interleaved, int nt) {
+    if (nt == 128) return interleaved ? q8_append_kernel<T, true, 128> : q8_append_kernel<T, false, 128>;
+    if (nt == 256) return interleaved ? q8_append_kernel<T, true, 256> : q8_append_kernel<T, false, 256>;
+    return interleaved ? q8_append_kernel<T, true, 512> : q8_append_kernel<T, false, 512>;
 }
 
 }  // namespace
@@ -259,17 +268,19 @@ int launch_q8_append(const RopeArgs& a, unsigned int* err, char* msg, size_t msg
     const int passes = a.q ? (a.H + heads_per_pass - 1) / heads_per_pass : 0;
     const int items_per_token = (passes + kQ8QPasses - 1) / kQ8QPasses;
     const int64_t q_items = k.total_new * items_per_token;
-    const int64_t grid = page_ctas + (q_items + kQ8Threads / 32 - 1) / (kQ8Threads / 32);
+    // as many threads as hold a page's new tokens in registers, where that many can be had
+    const int64_t most = std::min<int64_t>(k.P, k.total_new) * units;
+    const int nt = most <= 128 * kQ8Held ? 128 : most <= 256 * kQ8Held ? 256 : 512;
+    const int64_t grid = page_ctas + (q_items + nt / 32 - 1) / (nt / 32);
     if (grid > 0x7fffffff) {
         snprintf(msg, msg_len, "q8 append: %lld CTAs exceed one launch", (long long)grid);
         return PA_ERR_UNSUPPORTED;
     }
     NvtxRange nv("pa::q8_append_kernel");
     timer_begin(PA_KC_APPEND, k.stream);
-    const bool bf16 = a.dtype == PA_BF16;
-    auto kern = bf16 ? (a.interleaved ? q8_append_kernel<__nv_bfloat16, true> : q8_append_kernel<__nv_bfloat16, false>)
-                     : (a.interleaved ? q8_append_kernel<__half, true> : q8_append_kernel<__half, false>);
-    kern<<<(unsigned)grid, kQ8Threads, 0, k.stream>>>(a, page_ctas, passes, items_per_token, q_items, err);
+    auto kern = a.dtype == PA_BF16 ? q8_append_kernel_of<__nv_bfloat16>(a.interleaved, nt)
+                                   : q8_append_kernel_of<__half>(a.interleaved, nt);
+    kern<<<(unsigned)grid, nt, 0, k.stream>>>(a, page_ctas, passes, items_per_token, q_items, err);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "q8 append launch: %s", cudaGetErrorString(e));

@@ -87,15 +87,14 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
 }
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
     float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr));
     return v;
 }
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
     return v;
 }
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -629,19 +628,23 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
             const int n_part = p.cluster * C::KW;
             auto part = [&](int k) { return (rg * C::KW + k % C::KW); };
             float mm0 = -INFINITY, mm1 = -INFINITY, L0 = 0.f, L1 = 0.f;
+#pragma unroll 4
             for (int k = 0; k < n_part; ++k) {
                 const float4 ml = ld_cluster_f4(cluster_addr(&xml[part(k) * 32 + lane], k / C::KW));
-                const float a0 = fmaxf(mm0, ml.x), a1 = fmaxf(mm1, ml.y);
-                const float v0 = a0 == -INFINITY ? 0.f : a0, v1 = a1 == -INFINITY ? 0.f : a1;
-                L0 = L0 * fast_exp2(mm0 - v0) + ml.z * fast_exp2(ml.x - v0);
-                L1 = L1 * fast_exp2(mm1 - v1) + ml.w * fast_exp2(ml.y - v1);
-                mm0 = a0;
-                mm1 = a1;
+                mm0 = fmaxf(mm0, ml.x);
+                mm1 = fmaxf(mm1, ml.y);
             }
             const float w0 = mm0 == -INFINITY ? 0.f : mm0, w1 = mm1 == -INFINITY ? 0.f : mm1;
+#pragma unroll 4
+            for (int k = 0; k < n_part; ++k) {
+                const float4 ml = ld_cluster_f4(cluster_addr(&xml[part(k) * 32 + lane], k / C::KW));
+                L0 = fmaf(ml.z, fast_exp2(ml.x - w0), L0);
+                L1 = fmaf(ml.w, fast_exp2(ml.y - w1), L1);
+            }
             const float inv0 = L0 == 0.f ? 0.f : 1.f / L0, inv1 = L1 == 0.f ? 0.f : 1.f / L1;
             for (int u = split * C::KW + kq; u < DP / 16; u += n_part) {
                 float x[2][4] = {};
+#pragma unroll 2
                 for (int k = 0; k < n_part; ++k) {
                     const float4 ml = ld_cluster_f4(cluster_addr(&xml[part(k) * 32 + lane], k / C::KW));
                     const float4 ev = ld_cluster_f4(cluster_addr(&xo[(part(k) * (DP / 8) + 2 * u) * 32 + lane], k / C::KW));
@@ -1048,15 +1051,19 @@ __device__ __forceinline__ bool decode_q8_few_rows(const CUtensorMap& tm_k, cons
         if (bad == 0 && mine) {
             const int n_part = p.cluster * NW;
             float mm = -INFINITY, L = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < n_part; ++k)
+                mm = fmaxf(mm, ld_cluster_f2(cluster_addr(&xml[(k % NW) * 32 + lane], k / NW)).x);
+            const float um = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 8
             for (int k = 0; k < n_part; ++k) {
                 const float2 ml = ld_cluster_f2(cluster_addr(&xml[(k % NW) * 32 + lane], k / NW));
-                const float a = fmaxf(mm, ml.x), v = a == -INFINITY ? 0.f : a;
-                L = L * fast_exp2(mm - v) + ml.y * fast_exp2(ml.x - v);
-                mm = a;
+                L = fmaf(ml.y, fast_exp2(ml.x - um), L);
             }
-            const float um = mm == -INFINITY ? 0.f : mm, iv = L == 0.f ? 0.f : 1.f / L;
+            const float iv = L == 0.f ? 0.f : 1.f / L;
             for (int n = split * NW + warp; n < DP / 8; n += n_part) {
                 float x0 = 0.f, x1 = 0.f;
+#pragma unroll 8
                 for (int k = 0; k < n_part; ++k) {
                     const float2 ml = ld_cluster_f2(cluster_addr(&xml[(k % NW) * 32 + lane], k / NW));
                     const float2 v = ld_cluster_f2(cluster_addr(&xo[((k % NW) * (DP / 8) + n) * 32 + lane], k / NW));
