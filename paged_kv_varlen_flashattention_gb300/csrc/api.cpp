@@ -868,6 +868,19 @@ SplitPlan plan_splitkv(const Args& a, bool prefill_takes_long_rows, int prefill_
     return pl;
 }
 
+// Whether longer rows go to the 8-bit prefill kernel.  A call of few row tiles (one wave of them at two
+// CTAs an SM, from its sizes) and at most 1,024 keys stays with the split-KV kernel alone: one launch, and
+// on the device, 32 / 8 heads of 128, 18.8 to 15.5 us for 64 tokens, 23.0 to 19.3 for 256, 18.9 to 17.2
+// for four times 64; past either limit the prefill kernel is ahead (four times 256: 23.9 against 58.1;
+// 256 tokens over 4,256 keys: 80.5 against 95.7).  PA_Q8_ROW_TILES=0, read per call, switches this off.
+bool prefill_q8_wanted(const Args& a, int num_sms) {
+    if (!prefill_q8_supported(a)) return false;
+    const char* env = std::getenv("PA_Q8_ROW_TILES");
+    if (env && env[0] == '0') return true;
+    const int64_t row_tiles = ((int64_t)a.max_sq * (a.H / a.Hkv) + 31) / 32;
+    return a.max_sk > 1024 || (int64_t)a.batch * a.Hkv * row_tiles > 2 * num_sms;
+}
+
 SplitPlan plan_q8(const Args& a, bool prefill_takes_long_rows, int prefill_sms, int num_sms) {
     SplitPlan pl{};
     pl.dp = a.D <= 64 ? 64 : a.D <= 128 ? 128 : a.D <= 256 ? 256 : 512;
@@ -972,7 +985,7 @@ int launch_forward(pa::Args& a, void* stream, ScratchFn scratch, void* scratch_c
     int ce = pa::error_word(&err);
     if (ce != cudaSuccess) return fail(PA_ERR_CUDA, "error word: %s", cudaGetErrorString((cudaError_t)ce));
 
-    const bool use_prefill = a.k_scale ? pa::prefill_q8_supported(a) : pa::prefill_supported(a);
+    const bool use_prefill = a.k_scale ? pa::prefill_q8_wanted(a, sm_count()) : pa::prefill_supported(a);
     const auto launch_prefill = a.k_scale ? pa::launch_prefill_q8 : pa::launch_prefill;
     // SMs the persistent prefill grid may hold beside the decode-class pass (it runs before
     // that pass, not beside it, when there is no side stream)

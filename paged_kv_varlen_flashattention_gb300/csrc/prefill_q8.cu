@@ -160,6 +160,11 @@ __global__ void __launch_bounds__(kPqThreads, 1)
         if (lane == 0) mbar_arrive(&item_free[k & 1]);
         return true;
     };
+    // First key of step j of an item.  Under a bias the nearest keys come first: the score falls with
+    // the distance, so the reference stands from the first tiles on; in ascending order it would grow,
+    // and the accumulator be rescaled, at almost every tile (256 queries over 4,256 keys, 15 heads of
+    // 96: 121 us in ascending order, 109 so; unbiased 81).
+    auto tile_key = [&](const PfItem& it, int j) { return it.kt0 + (ALIBI ? it.n_tiles - 1 - j : j) * 128; };
     // The item's key tiles into the K ring (with the scales of each tile's four 32-key groups) or the V
     // ring.  Lane i holds the block id (and scales) of box i of a window of 32 boxes.
     auto produce = [&](const PfItem& it, const CUtensorMap* map, uint8_t* ring, uint64_t* fullb, uint64_t* emptyb,
@@ -171,7 +176,8 @@ __global__ void __launch_bounds__(kPqThreads, 1)
         for (int j = 0; j < it.n_tiles; ++j) {
             if (j >= jw + win_tiles) {
                 jw = j;
-                const int key = it.kt0 + j * 128 + lane * p.box_rows;
+                const int jl = j + lane / bpt;
+                const int key = jl < it.n_tiles ? tile_key(it, jl) + lane % bpt * p.box_rows : it.sk;
                 id = box_block(bt_row, p.bt_cols, p.num_blocks, p.P, key, it.sk, p.err);
                 if (scales && id >= 0) {
                     ksc = __ldg(p.ks + (int64_t)id * p.ks_s0 + (int64_t)it.hk * p.ks_s1);
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(kPqThreads, 1)
 #pragma unroll
                 for (int jj = 0; jj < 4; ++jj) {
                     if (blk[jj] < 0) continue;
-                    const int key = it.kt0 + j * 128 + jj * p.box_rows;
+                    const int key = tile_key(it, j) + jj * p.box_rows;
                     tma_load_4d(ring + s * C::TILE + jj * p.box_rows * 128, map, &fullb[s], 0, it.hk,
                                 key - (key / p.P) * p.P, blk[jj], 0ull);
                 }
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                 if (g >= 2 && !(ok = wait_all(&vc_empty[c], ((g >> 1) - 1) & 1))) break;
                 const uint8_t* src = smem + C::OFF_VR + s * C::TILE;
                 uint8_t* dst = smem + C::OFF_VC + c * C::VC_TILE;
-                const int kt = it.kt0 + j * 128;
+                const int kt = tile_key(it, j);
                 constexpr int UPR = DP / 16;          // 16-byte units of a row
                 constexpr int RPP = 32 / UPR;         // rows a warp converts a pass
                 const int uu = lane % UPR;
@@ -553,13 +559,15 @@ __global__ void __launch_bounds__(kPqThreads, 1)
             }
             const int64_t diag = qrow + ((int64_t)it.sk - it.sq);
             const int lo = p.wl >= 0 ? (int)max64(0, diag - p.wl) : 0;
-            const int hi = !live ? -1 : p.wr >= 0 ? (int)max64(-1, min64((int64_t)it.sk - 1, diag + p.wr)) : it.sk - 1;
+            // (rows past the tile's queries keep the mask of the query they would be: one that is empty
+            // would send their whole warp through the masked path at every tile: 81 to 138 us)
+            const int hi = p.wr >= 0 ? (int)max64(-1, min64((int64_t)it.sk - 1, diag + p.wr)) : it.sk - 1;
             const float ab = ALIBI && live ? p.alibi[h] * kLog2e : 0.f;
             float m = -INFINITY, l = 0.f, sl = 0.f;
 
             // One key tile: S -> running reference -> (rare) O rescale -> P.
             auto step = [&](int j) -> bool {
-                const int kt = it.kt0 + j * 128;
+                const int kt = tile_key(it, j);
                 if (!__all_sync(0xffffffffu, wait_bar(&s_full[x], (sx + j) & 1, abort_flag, p.err, p.wait_ns))) return false;
                 tc::fence_after_sync();
                 const float* slot = sc_ring + ((gk + j) % C::SC_RING) * 12;
@@ -588,10 +596,25 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                     c = fmaxf(sl * slot[2 * hb + g], 1e-37f);
                     lv = slot[4 + 2 * hb + g];
                 };
-                auto bias = [&](int hb, int g, float c, float lv, float(&v)[32]) {  // the whole x of a biased score
-                    const float d0 = (float)((int)diag - kt - 64 * hb - 32 * g);
+                // the whole x of a biased score: x = c v - ab |diag - key| + add, two keys at a time where
+                // no row has live keys on both sides of its own position (the same call: 144 us key by key)
+                const bool above = kt >= diag;
+                const bool one_sided = ALIBI && __all_sync(0xffffffffu, above || kt + 127 <= diag || hi <= diag);
+                auto bias = [&](int hb, int g, float c, float add, float(&v)[32]) {
+                    float d0 = (float)((int)diag - kt - 64 * hb - 32 * g);
+                    if (one_sided) {
+                        const float na = above ? ab : -ab;
+                        float d1 = d0 - 1.f;
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = fmaf(-ab, fabsf(d0 - (float)i), fmaf(v[i], c, lv));
+                        for (int i = 0; i < 32; i += 2) {
+                            ffma2(v[i], v[i + 1], v[i], v[i + 1], c, c, add, add);
+                            ffma2(v[i], v[i + 1], d0, d1, na, na, v[i], v[i + 1]);
+                            fadd2_acc(d0, d1, -2.f, -2.f);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = fmaf(-ab, fabsf(d0 - (float)i), fmaf(v[i], c, add));
+                    }
                 };
                 float mx = -INFINITY;
 #pragma unroll 1

@@ -9,6 +9,11 @@ from tests.test_q8_attention_gpu import call, check, inputs, run
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(autouse=True)
+def _prefill_kernel_takes_small_calls(monkeypatch):
+    monkeypatch.setenv("PA_Q8_ROW_TILES", "0")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("D", [16, 48, 64, 80, 128])
 def test_prompts(D, dtype):
@@ -154,3 +159,23 @@ def test_withheld_loads_time_out():
 def test_row_tiles_without_the_tensor_core_kernel(monkeypatch):
     """The same rows on the split-KV kernel (scale <= 0 keeps them there) against the tensor-core one."""
     run([70, 129], [300, 129], D=128, scale=-0.1, seed=17)
+
+
+@pytest.mark.parametrize("alibi", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_small_calls_on_row_tiles(alibi, dtype, monkeypatch):
+    """Calls of few row tiles take the split-KV kernel: one sequence beside another, a group that does not
+    divide a tile, and the first sizes past the rule."""
+    monkeypatch.delenv("PA_Q8_ROW_TILES")
+    slopes = torch.exp2(-torch.arange(1, 11).float()) if alibi else None
+    for sq, sk in ([64], [64]), ([256], [300]), ([33, 1, 7], [1000, 1024, 0]), ([100], [1025]), ([400, 90], [400, 900]):
+        run(sq, sk, H=10, Hkv=2, D=96, P=96, dtype=dtype, slopes=slopes, seed=sum(sq))
+
+
+@pytest.mark.parametrize("wl,wr", [(-1, 0), (-1, -1), (200, 100), (0, 300)])
+def test_bias_over_many_tiles(wl, wr):
+    """Keys on one side of a query's position and on both, over tiles taken from the nearest on."""
+    run([300, 140], [1500, 333], H=10, Hkv=2, D=128, P=64, wl=wl, wr=wr,
+        slopes=torch.exp2(-torch.arange(1, 11).float()), seed=wl + 7)
+    run([260], [2300], H=4, Hkv=4, D=64, P=32, wl=wl, wr=wr, slopes=torch.tensor([1.0, 0.1, 0.01, 0.0]),
+        dtype="f16", seed=wl + 8)
