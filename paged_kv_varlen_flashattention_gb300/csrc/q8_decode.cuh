@@ -773,9 +773,46 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
 template <typename T>
 struct Q8Terms {
     static constexpr int N = std::is_same<T, __half>::value ? 3 : 2;
-    static constexpr int S = N == 2 ? 8 : 4;  // rows a unit can have
+    static constexpr int S = N == 2 ? 8 : 4;   // rows a unit can have
+    static constexpr int SW = N == 2 ? 4 : 2;  // with the terms in the product's columns
 };
 constexpr float kQ8TermOffset = 8.f;  // largest weight 2^8
+
+// The terms of a row of q, eight columns a lane, each term `pitch` bytes after the one before; sc takes
+// the power of two back out.  Whole warp.
+template <typename T>
+__device__ __forceinline__ void q8_store_terms(const uint4& x, bool store, uint8_t* dst, int pitch, float& sc) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    float v[8], mx = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 f = unpack2<T>(w[e]);
+        v[2 * e] = f.x;
+        v[2 * e + 1] = f.y;
+        mx = max3f(mx, fabsf(f.x), fabsf(f.y));
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+    // the largest power of two with mx 2^e2 <= 448 = 1.75 x 2^8; an infinite element makes the row NaN
+    const int bits = __float_as_int(mx);
+    const int e2 = min(126, 8 - ((bits >> 23) - 127) - ((bits & 0x7fffff) > 0x600000 ? 1 : 0));
+    const float up = mx <= 3.4028235e38f ? __int_as_float((127 + e2) << 23) : NAN;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= up;
+#pragma unroll
+    for (int t = 0; t < Q8Terms<T>::N; ++t) {
+        uint32_t c2[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            c2[e] = e4m3x2_take(v[2 * e], v[2 * e + 1]);
+            v[2 * e] *= 16.f;
+            v[2 * e + 1] *= 16.f;
+        }
+        if (store)
+            *reinterpret_cast<uint2*>(dst + t * pitch) = make_uint2(c2[0] | (c2[1] << 16), c2[2] | (c2[3] << 16));
+    }
+    sc = __int_as_float((127 - e2) << 23);
+}
 
 template <typename T, int DP, int NW, int NT, int STAGES, int ML>
 __device__ __forceinline__ bool decode_q8_few_rows(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Q8Params& p,
@@ -835,37 +872,9 @@ __device__ __forceinline__ bool decode_q8_few_rows(const CUtensorMap& tm_k, cons
 #pragma unroll
         for (int k = 0; k < S / NW; ++k) {
             const int r = warp + k * NW;
-            const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            float v[8], mx = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack2<T>(w[e]);
-                v[2 * e] = f.x;
-                v[2 * e + 1] = f.y;
-                mx = max3f(mx, fabsf(f.x), fabsf(f.y));
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            // the largest power of two with mx 2^e2 <= 448 = 1.75 x 2^8; an infinite element makes the row NaN
-            const int bits = __float_as_int(mx);
-            const int e2 = min(126, 8 - ((bits >> 23) - 127) - ((bits & 0x7fffff) > 0x600000 ? 1 : 0));
-            const float up = mx <= 3.4028235e38f ? __int_as_float((127 + e2) << 23) : NAN;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= up;
-#pragma unroll
-            for (int t = 0; t < NTERM; ++t) {
-                uint32_t c2[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    c2[e] = e4m3x2_take(v[2 * e], v[2 * e + 1]);
-                    v[2 * e] *= 16.f;
-                    v[2 * e + 1] *= 16.f;
-                }
-                if (lane * 8 < DP)
-                    *reinterpret_cast<uint2*>(qs + (t * S + r) * QP + lane * 8) =
-                        make_uint2(c2[0] | (c2[1] << 16), c2[2] | (c2[3] << 16));
-            }
-            if (lane == 0) rows.sc[r] = p.scale_log2 * __int_as_float((127 - e2) << 23);
+            float sc;
+            q8_store_terms<T>(x[k], lane * 8 < DP, qs + r * QP + lane * 8, S * QP, sc);
+            if (lane == 0) rows.sc[r] = p.scale_log2 * sc;
         }
     }
     named_barrier_sync(1, NW * 32);
@@ -1124,6 +1133,286 @@ __device__ __forceinline__ bool decode_q8_few_rows(const CUtensorMap& tm_k, cons
     return true;
 }
 
+// The same for at most 4 rows (bf16) or 2 (f16), a group of 4 heads or fewer for one token: all terms of
+// all rows fit the 8 columns of a product, so K and V are its 16-row operand and q and the weights the
+// other, and 32 keys of 128 columns take 16 products, half the softmax and half the accumulators.
+// Term t of row r is column TS r + t (TS = 2, or 4 with three terms): lane 4 g + t holds columns 2 t
+// and 2 t + 1, so of bf16 both terms of row t.
+//
+//   S^T = K q^T: keys are rows; lane 4 g + t has four keys of its row, k(g, j) = 8 j + (g + 2 j) % 8, j = 0..3.
+//   O^T = V^T w^T: columns of V are rows; the weights go through 256 bytes of shared memory a warp to
+//   get from a lane per key to a lane per column, as term words w(4 g + j) of keys k(g, j), and the rows of V
+//   are read in that order.  Both orders leave every eight rows of an ldmatrix in different banks.
+template <typename T, int DP, int NW, int NT, int STAGES, int ML>
+__device__ __forceinline__ bool decode_q8_swapped(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const Q8Params& p,
+                                                  uint8_t* smem, int b, int hk, int split, int g0, int& n_done) {
+    using C = Q8Cfg<DP, 1, NW, NT, STAGES, ML>;
+    constexpr int NTERM = Q8Terms<T>::N, TS = NTERM == 2 ? 2 : 4, S = Q8Terms<T>::SW;
+    constexpr int QP = DP + 16;            // q column pitch: eight columns of a fragment load in different banks
+    constexpr int WP = 12;                 // words between the columns of a warp's weights, likewise
+    constexpr int OFF_W = C::OFF_Q + 8 * QP;
+    static_assert(C::KPW == 32 && S <= NW && 8 * QP + NW * 8 * WP * 4 <= 16 * ML * C::QP, "shared memory of q");
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    TileView tv;
+    n_done = 0;
+    if (!tile_view<16, NT>(p, b, 0, tv, split == 0)) return false;
+    bool single;
+    int t_begin, n_iter;
+    if (!q8_tiles(p, tv, split, t_begin, n_iter, single)) return false;
+    n_done = n_iter;
+    const int kbeg = tv.kt0 + t_begin * NT;
+
+    const Q8Rows rows = q8_rows(smem + C::OFF_ROW, 16);
+    uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* k_empty = k_full + STAGES;
+    uint64_t* v_full = k_empty + STAGES;
+    uint64_t* v_empty = v_full + STAGES;
+    volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG);
+    q8_row_bounds(p, tv, rows, hk, 16);
+    __syncthreads();  // rows, and for a CTA's first unit the barriers
+
+    if (warp >= NW) {
+        int* ids = reinterpret_cast<int*>(smem + C::OFF_IDS);
+        if (warp == NW)
+            q8_produce<DP, NT, STAGES>(p, &tm_k, smem, k_full, k_empty, ids, true, b, hk, tv.sk, kbeg, n_iter, g0, abort_flag);
+        else
+            q8_produce<DP, NT, STAGES>(p, &tm_v, smem + C::OFF_V, v_full, v_empty, ids + kQ8MaxBoxes, false, b, hk, tv.sk,
+                                       kbeg, n_iter, g0, abort_flag);
+        if (p.cluster > 1) q8_cluster_passive();
+        return true;
+    }
+    auto block_key = [&](int n) { return kbeg + n * NT + warp * 32; };  // 32 aligned keys lie in one page
+    Q8Scales scales;
+    scales.fetch(p, b, hk, tv.sk, 0, n_iter, block_key);
+    uint8_t* qs = smem + C::OFF_Q;
+    if (warp < S) {  // q in its terms, a row a warp; rows without a query are zero
+        const int r = warp, i = r / p.G, g = r - i * p.G;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < tv.rows && lane * 8 < p.D)
+            x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (int64_t)(tv.q0 + i) * p.q_s0 +
+                                                     (int64_t)(hk * p.G + g) * p.q_s1 + lane * 8));
+        float sc;
+        q8_store_terms<T>(x, lane * 8 < DP, qs + r * TS * QP + lane * 8, QP, sc);
+        if (TS > NTERM && lane * 8 < DP) *reinterpret_cast<uint2*>(qs + (r * TS + NTERM) * QP + lane * 8) = make_uint2(0, 0);
+        if (lane == 0) rows.sc[r] = p.scale_log2 * sc;
+    }
+    named_barrier_sync(1, NW * 32);
+
+    const int gq = lane >> 2, tq = lane & 3;
+    const int mi = lane >> 3, rr = lane & 7;
+    const int row = TS == 2 ? tq : tq >> 1;
+    const bool first = TS == 2 || (tq & 1) == 0;  // holds terms 0 and 1 (and not term 2)
+    const int lo = rows.lo[row], hi = rows.hi[row], dg = rows.dg[row];
+    const float ab = rows.ab[row], cs = rows.sc[row];
+    int plain_lo = lo, plain_hi = hi;
+    q8_plain_keys(p.alibi != nullptr, plain_lo, plain_hi);
+    uint32_t qf[DP / 32][2];
+#pragma unroll
+    for (int ks = 0; ks < DP / 32; ++ks) {
+        qf[ks][0] = *reinterpret_cast<const uint32_t*>(qs + gq * QP + ks * 32 + tq * 4);
+        qf[ks][1] = *reinterpret_cast<const uint32_t*>(qs + gq * QP + ks * 32 + 16 + tq * 4);
+    }
+    auto key_at = [](int g, int j) { return 8 * j + ((g + 2 * j) & 7); };
+    auto sum_terms = [&](float c0, float c1) { return first ? fmaf(c1, 1.f / 16.f, c0) : c0 * (1.f / 256.f); };
+    uint32_t* wbuf = reinterpret_cast<uint32_t*>(smem + OFF_W) + warp * 8 * WP;
+    float o[DP / 16][4];  // columns 16 u + gq and + 8 of V, this lane's two terms each
+#pragma unroll
+    for (int u = 0; u < DP / 16; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[u][e] = 0.f;
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+
+    const int key0 = warp * 32, v_row = key0 + key_at(lane >> 2, lane & 3);
+    for (int it = 0; ok && it < n_iter; ++it) {
+        const int gi = g0 + it, stage = gi % STAGES;
+        const uint32_t par = (gi / STAGES) & 1;
+        const int kt = kbeg + it * NT + key0;  // the warp's first key
+        ok = __all_sync(0xffffffffu, q8_wait(&k_full[stage], par, abort_flag, p.err, p.wait_ns));
+        if (!ok) break;
+        const uint32_t k_base = smem_addr(smem + stage * C::TILE), v_base = smem_addr(smem + C::OFF_V + stage * C::TILE);
+        float kss, lv;
+        scales.take(p, b, hk, tv.sk, it, n_iter, block_key, kss, lv);
+        kss *= cs;
+        float s[2][2][4];  // [chain][16-key tile]
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[c][h][e] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < DP / 32; ++ks)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t a[4];
+                ldsm_x4(k_base + q8_off<DP, NT>(key0 + key_at(rr, 2 * h + (mi & 1)), 2 * ks + (mi >> 1)), a[0], a[1], a[2], a[3]);
+                mma_e4m3(s[ks & 1][h], a, qf[ks][0], qf[ks][1]);
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&k_empty[stage]);
+        float x[4];  // of keys k(gq, j)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int h = j >> 1, e = 2 * (j & 1);
+            x[j] = sum_terms(s[0][h][e] + s[1][h][e], s[0][h][e + 1] + s[1][h][e + 1]);
+            if (TS == 4) x[j] += __shfl_xor_sync(0xffffffffu, x[j], 1);
+        }
+        if (kt >= plain_lo && kt + 31 <= plain_hi) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] = fmaf(x[j], kss, lv);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int key = kt + key_at(gq, j);
+                x[j] = q8_score(x[j], kss, lv, key >= lo && key <= hi, ab, dg, key);
+            }
+        }
+        float mx = max3f(x[0], x[1], fmaxf(x[2], x[3]));
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        if (__any_sync(0xffffffffu, mx > m)) {
+            const float nm = fmaxf(m, mx);
+            const float f = nm == -INFINITY ? 1.f : fast_exp2(m - nm);
+            m = nm;
+            l *= f;
+#pragma unroll
+            for (int u = 0; u < DP / 16; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[u][e] *= f;
+        }
+        const float ref = m == -INFINITY ? 0.f : m - kQ8TermOffset;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[j] = fast_exp2(x[j] - ref);
+            sum += x[j];
+        }
+        l = fmaf(sum, fast_exp2(-lv), l);
+        uint32_t t[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int k = 0; k < NTERM; ++k) {
+            const uint32_t c0 = e4m3x2_take(x[0], x[1]), c1 = e4m3x2_take(x[2], x[3]);
+            t[k] = c0 | (c1 << 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[j] *= 16.f;
+        }
+        wbuf[2 * tq * WP + gq] = first ? t[0] : t[2];
+        wbuf[(2 * tq + 1) * WP + gq] = first ? t[1] : 0u;
+        __syncwarp();
+        const uint32_t w0 = wbuf[gq * WP + tq], w1 = wbuf[gq * WP + 4 + tq];
+        ok = __all_sync(0xffffffffu, q8_wait(&v_full[stage], par, abort_flag, p.err, p.wait_ns));
+        if (!ok) break;
+        // V rows of this warp's keys that no row attends become 0 (0 x NaN is NaN): keys before the first
+        // interval, past the last, and slots that were never loaded
+        const bool zeroed = kt < tv.lo || kt + 31 > tv.hi;
+        if (zeroed) {
+            if (kt + lane < tv.lo || kt + lane > tv.hi) {
+                uint8_t* vst = smem + C::OFF_V + stage * C::TILE;
+#pragma unroll
+                for (int u = 0; u < DP / 16; ++u)
+                    *reinterpret_cast<uint4*>(vst + q8_off<DP, NT>(key0 + lane, u)) = make_uint4(0, 0, 0, 0);
+            }
+            __syncwarp();
+        }
+#pragma unroll
+        for (int u = 0; u < DP / 16; ++u) {
+            uint32_t a[4];
+            ldsm_b8_x2_t(v_base + q8_off<DP, NT>(v_row, u), a[0], a[1], a[2], a[3]);
+            mma_e4m3(o[u], a, w0, w1);
+        }
+        if (zeroed) fence_proxy_async_smem();  // the stage is rewritten by TMA later
+        __syncwarp();                          // (and the weights by the next step)
+        if (lane == 0) mbar_arrive(&v_empty[stage]);
+    }
+
+    // ---- sum the terms, then merge the key slices of the warps (and of the cluster's CTAs) ----
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    const bool gave_up = named_barrier_or(1, NW * 32, !ok || *abort_flag != 0u);
+    if (gave_up && p.cluster <= 1) return true;  // all leave together
+    constexpr int OP = DP + 8;                           // row pitch of a warp's sums
+    float* xo = reinterpret_cast<float*>(smem);          // [warp][row][column], in the rings
+    float2* xml = reinterpret_cast<float2*>(xo + NW * S * OP);  // [warp][row]: m, l
+#pragma unroll
+    for (int u = 0; u < DP / 16; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float v = sum_terms(o[u][2 * e], o[u][2 * e + 1]);
+            if (TS == 4) v += __shfl_xor_sync(0xffffffffu, v, 1);
+            if (first) xo[(warp * S + row) * OP + 16 * u + 8 * e + gq] = v;
+        }
+    if (gq == 0 && first) xml[warp * S + row] = make_float2(m, l);
+    auto emit = [&](int r, int d, float mm, float L, float x0, float x1) {
+        const int i = r / p.G, h = hk * p.G + (r - i * p.G);
+        const int64_t t = tv.q0 + i;
+        if (single)
+            *reinterpret_cast<uint32_t*>(static_cast<T*>(p.out) + t * p.o_s0 + (int64_t)h * p.o_s1 + d) = pack2<T>(x0, x1);
+        else
+            *reinterpret_cast<float2*>(p.part_o + ((int64_t)split * p.part_stride + t * p.H + h) * p.D + d) =
+                make_float2(x0, x1);
+        if (d == 0) {
+            const float lse = L == 0.f ? -INFINITY : (mm - kQ8TermOffset + log2f(L)) * 0.69314718055994531f;
+            if (single)
+                p.lse[(int64_t)h * p.lse_s0 + t + (int64_t)b * p.lse_sb] = lse;
+            else
+                p.part_lse[(int64_t)split * p.part_stride + t * p.H + h] = lse;
+        }
+    };
+    if (p.cluster > 1) {
+        if (gave_up && tid == 0) *abort_flag = 1u;
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        uint32_t bad = 0;
+        for (int c = 0; c < p.cluster; ++c) bad |= ld_cluster_u32(cluster_addr(const_cast<uint32_t*>(abort_flag), c));
+        const int n_part = p.cluster * NW;
+        for (int i = tid * p.cluster + split; bad == 0 && i < S * DP / 2; i += NW * 32 * p.cluster) {
+            const int r = i / (DP / 2), d = i % (DP / 2) * 2;
+            if (r >= tv.rows || d >= p.D) continue;
+            float mm = -INFINITY, L = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll 8
+            for (int k = 0; k < n_part; ++k) mm = fmaxf(mm, ld_cluster_f2(cluster_addr(&xml[k % NW * S + r], k / NW)).x);
+            const float um = mm == -INFINITY ? 0.f : mm;
+#pragma unroll 8
+            for (int k = 0; k < n_part; ++k) {
+                const float2 ml = ld_cluster_f2(cluster_addr(&xml[k % NW * S + r], k / NW));
+                const float2 v = ld_cluster_f2(cluster_addr(&xo[(k % NW * S + r) * OP + d], k / NW));
+                const float f = fast_exp2(ml.x - um);
+                L = fmaf(ml.y, f, L);
+                x0 = fmaf(f, v.x, x0);
+                x1 = fmaf(f, v.y, x1);
+            }
+            const float iv = L == 0.f ? 0.f : 1.f / L;
+            emit(r, d, mm, L, x0 * iv, x1 * iv);
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+        return true;
+    }
+    named_barrier_sync(1, NW * 32);
+    for (int i = tid; i < S * DP / 2; i += NW * 32) {
+        const int r = i / (DP / 2), d = i % (DP / 2) * 2;
+        if (r >= tv.rows || d >= p.D) continue;
+        float mm = -INFINITY, L = 0.f, x0 = 0.f, x1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) mm = fmaxf(mm, xml[k * S + r].x);
+        const float um = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) {
+            const float2 ml = xml[k * S + r], v = *reinterpret_cast<const float2*>(&xo[(k * S + r) * OP + d]);
+            const float f = fast_exp2(ml.x - um);
+            L = fmaf(ml.y, f, L);
+            x0 = fmaf(f, v.x, x0);
+            x1 = fmaf(f, v.y, x1);
+        }
+        const float iv = L == 0.f ? 0.f : 1.f / L;
+        emit(r, d, mm, L, x0 * iv, x1 * iv);
+    }
+    return true;
+}
+
 // The sequence of a grid index: longest first (order from a ranking pass, or ranked here).
 __device__ __forceinline__ int q8_sequence(const SplitParams& p, int* rank_len, int* rank_pick) {
     const int z = (int)blockIdx.z, tid = threadIdx.x;
@@ -1171,14 +1460,17 @@ __global__ void __launch_bounds__(NW * 32 + 64, 2)
     // A sequence of few rows runs on the body for them, and in a kernel for two row groups one of at
     // most 16 rows on the one-group body.
     auto run_unit = [&](int b, int hk, int rt, int split, int g0, int& n_done) -> bool {
-        if (rt == 0 && b >= 0 && b < p.batch && (int64_t)(p.cu_q[b + 1] - p.cu_q[b]) * p.G <= Q8Terms<T>::S)
+        const int64_t n_rows = b >= 0 && b < p.batch ? (int64_t)(p.cu_q[b + 1] - p.cu_q[b]) * p.G : INT32_MAX;
+        if (rt == 0 && n_rows <= Q8Terms<T>::SW)
+            return decode_q8_swapped<T, DP, NW, NT, STAGES, MG>(tm_k, tm_v, p, smem, b, hk, split, g0, n_done);
+        if (rt == 0 && n_rows <= Q8Terms<T>::S)
             return decode_q8_few_rows<T, DP, NW, NT, STAGES, MG>(tm_k, tm_v, p, smem, b, hk, split, g0, n_done);
         if constexpr (MG == 2) {
             using L1 = Q8Cfg<DP, 1, NW, NT, STAGES, 2>;
             static_assert(L1::OFF_ROW == C::OFF_ROW && L1::OFF_BAR == C::OFF_BAR && L1::OFF_IDS == C::OFF_IDS &&
                               L1::SMEM == C::SMEM,
                           "both bodies share one shared-memory layout");
-            if (b >= 0 && b < p.batch && (int64_t)(p.cu_q[b + 1] - p.cu_q[b]) * p.G <= 16)
+            if (n_rows <= 16)
                 return decode_q8_unit<T, DP, 1, NW, NT, STAGES, 2>(tm_k, tm_v, p, smem, b, hk, rt, split, g0, n_done);
         }
         return decode_q8_unit<T, DP, MG, NW, NT, STAGES, MG>(tm_k, tm_v, p, smem, b, hk, rt, split, g0, n_done);
