@@ -16,7 +16,7 @@ LIB = os.path.join(PKG, "libpa_varlen.so")
 
 SOURCES = ["api.cpp", "errword.cu", "splitkv_bf16.cu", "splitkv_f16.cu", "prefill_tc.cu", "decode_tc.cu", "noalloc.cu",
            "kv_append.cu", "padded.cu", "rope_append.cu", "q8_append.cu",
-           "q8_bf16.cu", "q8_f16.cu", "prefill_q8.cu"]
+           "q8_bf16.cu", "q8_f16.cu", "prefill_q8.cu", "prefill_q8_wide.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -34,7 +34,7 @@
 #include <cstdlib>
 #include <type_traits>
 
-#include "prefill_common.cuh"
+#include "prefill_q8_common.cuh"
 #include "q8_common.cuh"
 #include "rope_common.cuh"
 
@@ -46,12 +46,6 @@ constexpr int kPqThreads = 512;
 // 128 x 96 + 256 x 152 + 128 x 112 = 65,536.  (56 / 192 / 72 spilled in the issuers: 7 % slower.)
 constexpr int kPqRegsControl = 96, kPqRegsSoftmax = 152, kPqRegsConvert = 112;
 constexpr float kPqOffset = 7.f;
-
-struct PrefillQ8Params : PrefillParams {
-    const float* ks;
-    const float* vs;
-    int64_t ks_s0, ks_s1, vs_s0, vs_s1;
-};
 
 // DP: padded head dim, 64 or 128 (rows of the 8-bit tiles are 128 bytes either way, zero filled
 // past the head dim); NTERM: e4m3 terms of q.
@@ -740,17 +734,14 @@ template <typename T, int DP, bool ALIBI>
 int run_prefill_q8(const Args& a, const PrefillQ8Params& pp, char* msg, size_t msg_len) {
     constexpr int SMEM = PqCfg<DP, std::is_same<T, __half>::value ? 3 : 2>::SMEM;
     auto kern = prefill_q8_kernel<T, DP, ALIBI>;
-    static int sms = 0;
-    if (!sms) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-        int dev = 0, n = 0;
-        if (e == cudaSuccess) e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e != cudaSuccess) {
-            snprintf(msg, msg_len, "configuring the q8 prefill (%d bytes of shared memory): %s", SMEM, cudaGetErrorString(e));
-            return PA_ERR_CUDA;
-        }
-        sms = n;
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0, sms = 0;
+    cudaError_t e = set_shared_memory(kern, SMEM, configured);
+    if (e == cudaSuccess) e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) {
+        snprintf(msg, msg_len, "configuring the q8 prefill (%d bytes of shared memory): %s", SMEM, cudaGetErrorString(e));
+        return PA_ERR_CUDA;
     }
     if ((int64_t)pp.pairs * a.Hkv + sms >= (int64_t)INT32_MAX) {
         snprintf(msg, msg_len, "q8 prefill: %lld work items (tiles x kv heads) exceed the item counter's range",
@@ -769,7 +760,7 @@ int run_prefill_q8(const Args& a, const PrefillQ8Params& pp, char* msg, size_t m
     if (rc == PA_OK) rc = encode_tmap_4d(&tv, PA_E4M3, a.v, dims, strides, box, 1, msg, msg_len);
     if (rc != PA_OK) return rc;
     NvtxRange nv("pa::prefill_q8_kernel");
-    cudaError_t e = cudaMemsetAsync(pp.counter, 0, sizeof(int), a.stream);
+    e = cudaMemsetAsync(pp.counter, 0, sizeof(int), a.stream);
     if (e != cudaSuccess) {
         snprintf(msg, msg_len, "q8 prefill: zeroing the item counter: %s", cudaGetErrorString(e));
         return PA_ERR_CUDA;
@@ -794,56 +785,17 @@ int launch_prefill_q8_t(const Args& a, const PrefillQ8Params& pp, char* msg, siz
 
 }  // namespace
 
-// Long queries of these calls go to the kernel above (the same conditions as the 16-bit kernels',
-// up to the head dim).
-bool prefill_q8_supported(const Args& a) { return a.D <= 128 && prefill_supported(a); }
+// Long queries of these calls go to the kernel above or, beyond head_dim 128, to prefill_q8_wide.cu's (the
+// same conditions as the 16-bit kernels').
+bool prefill_q8_supported(const Args& a) { return prefill_supported(a); }
 
 int launch_prefill_q8(const Args& a, int* counter, unsigned int* err, char* msg, size_t msg_len) {
+    if (a.D > 128) return launch_prefill_q8_wide(a, counter, err, msg, msg_len);
     if (!counter) {
         snprintf(msg, msg_len, "the prefill kernels need a device item counter");
         return PA_ERR_ARG;
     }
-    PrefillQ8Params pp{};
-    pp.counter = counter;
-    pp.out = a.out;
-    pp.o_s0 = a.o_s0;
-    pp.o_s1 = a.o_s1;
-    pp.lse = a.lse;
-    pp.lse_s0 = a.lse_s0;
-    pp.lse_sb = a.lse_sb;
-    pp.cu_q = a.cu_q;
-    pp.cu_k = a.cu_k;
-    pp.bt = a.block_table;
-    pp.bt_s0 = a.bt_s0;
-    pp.bt_cols = a.bt_cols;
-    pp.batch = a.batch;
-    pp.H = a.H;
-    pp.Hkv = a.Hkv;
-    pp.G = a.H / a.Hkv;
-    pp.D = a.D;
-    pp.P = a.page;
-    pp.num_blocks = a.num_blocks;
-    pp.total_q = a.total_q;
-    pp.paged = 1;
-    pp.max_sq = a.max_sq;
-    pp.max_sk = a.max_sk;
-    pp.scale_log2 = a.scale * 1.4426950408889634f;
-    pp.alibi = a.alibi;
-    pp.wl = a.wl;
-    pp.wr = a.wr;
-    pp.rows_cap = prefill_rows_threshold();
-    pp.err = err;
-    pp.wait_ns = a.wait_ns;
-    pp.withhold = a.withhold_loads;
-    pp.box_rows = a.page % 128 == 0 ? 128 : a.page % 64 == 0 ? 64 : 32;
-    pp.boxes_per_tile = 128 / pp.box_rows;
-    pp.pairs = (int)(prefill_items_bound(a) / a.Hkv);
-    pp.ks = a.k_scale;
-    pp.vs = a.v_scale;
-    pp.ks_s0 = a.ks_s0;
-    pp.ks_s1 = a.ks_s1;
-    pp.vs_s0 = a.vs_s0;
-    pp.vs_s1 = a.vs_s1;
+    const PrefillQ8Params pp = prefill_q8_params(a, counter, err, 128);
     return a.dtype == PA_BF16 ? launch_prefill_q8_t<__nv_bfloat16>(a, pp, msg, msg_len)
                               : launch_prefill_q8_t<__half>(a, pp, msg, msg_len);
 }

@@ -2,11 +2,25 @@
 // an element's value is code x scale.
 #pragma once
 
+#include <atomic>
 #include <cuda_fp16.h>
 
 #include "device_common.cuh"
 
 namespace pa {
+
+// Dynamic shared memory of a kernel, set once for each device that launches it.
+template <typename K>
+cudaError_t set_shared_memory(K kernel, int bytes, std::atomic<uint64_t>& devices) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (devices.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 constexpr float kE4m3Max = 448.f;
 constexpr int kScaleExpMin = -100;  // the smallest scale an append gives a page, and a read sees, is 2^-100

@@ -53,20 +53,16 @@ template <typename T, int DP, int MG>
 static int run_q8(const CUtensorMap& tk, const CUtensorMap& tv, const Q8Params& sp, const SplitPlan& plan,
                   cudaStream_t stream, char* msg, size_t msg_len) {
     using K = Q8Kernel<T, DP, MG>;
-    static bool configured = false;
-    if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(K::kernel(), cudaFuncAttributeMaxDynamicSharedMemorySize, K::C::SMEM);
-        if (e != cudaSuccess) {
-            snprintf(msg, msg_len, "cudaFuncSetAttribute(q8 decode, %d bytes): %s", K::C::SMEM, cudaGetErrorString(e));
-            return PA_ERR_CUDA;
-        }
-        configured = true;
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t e = set_shared_memory(K::kernel(), K::C::SMEM, configured);
+    if (e != cudaSuccess) {
+        snprintf(msg, msg_len, "cudaFuncSetAttribute(q8 decode, %d bytes): %s", K::C::SMEM, cudaGetErrorString(e));
+        return PA_ERR_CUDA;
     }
     if (sp.order) {
         const int rc = launch_longest_first(sp.cu_k, sp.batch, const_cast<int*>(sp.order), stream, msg, msg_len);
         if (rc != PA_OK) return rc;
     }
-    cudaError_t e;
     if (sp.work) {
         NvtxRange nvw("pa::work_list_kernel");
         work_list_kernel<K::C::M, K::NT><<<1, kMaxOrderBatch, 0, stream>>>(sp, sp.work);

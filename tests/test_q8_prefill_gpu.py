@@ -179,3 +179,43 @@ def test_bias_over_many_tiles(wl, wr):
         slopes=torch.exp2(-torch.arange(1, 11).float()), seed=wl + 7)
     run([260], [2300], H=4, Hkv=4, D=64, P=32, wl=wl, wr=wr, slopes=torch.tensor([1.0, 0.1, 0.01, 0.0]),
         dtype="f16", seed=wl + 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [144, 192, 208, 256])
+def test_wide_prompts(D, dtype):
+    run([33, 64, 129, 257], [33, 64, 129, 257], H=2, Hkv=1, D=D, dtype=dtype, seed=D)
+
+
+@pytest.mark.parametrize("H,Hkv", [(1, 1), (3, 1), (4, 4), (10, 2), (64, 1)])
+def test_wide_group_sizes(H, Hkv):
+    run([90, 40, 300 // (H // Hkv) + 33], [90, 200, 400], H=H, Hkv=Hkv, D=256, seed=H)
+
+
+@pytest.mark.parametrize("m", [1, 31, 32, 63, 64, 65, 127, 128, 129, 193])
+def test_wide_key_tile_borders(m):
+    """One, two and three key tiles, and a last one that is not full."""
+    run([max(1, m // 2), 40], [m, max(40, m)], H=8, Hkv=1, D=256, seed=m)
+
+
+@pytest.mark.parametrize("wl,wr,slopes", [(0, 0, False), (100, 0, True), (-1, -1, True), (63, 64, False), (300, -1, True),
+                                          (-1, 60, False)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_wide_windows(wl, wr, slopes, dtype):
+    run([200, 50, 33], [500, 50, 390], wl=wl, wr=wr, H=4, Hkv=2, D=192, P=96, dtype=dtype, seed=wl + 301,
+        slopes=torch.tensor([1.0, 0.1, 0.01, 0.0]) if slopes else None)
+
+
+@pytest.mark.parametrize("P", [32, 64, 96, 256])
+def test_wide_page_sizes(P):
+    run([140, 70], [300, 1313], D=256, P=P, H=4, Hkv=2, seed=P, kind="absmax")
+
+
+def test_wide_items_follow_each_other():
+    """Many short items on every CTA, some without keys, one and several key tiles in any order; rows of
+    large scores late in a sequence, which raise the reference."""
+    g = torch.Generator().manual_seed(17)
+    sq = torch.randint(17, 200, (230,), generator=g).tolist()
+    sk = [m + int(torch.randint(0, 200, (1,), generator=g)) if i % 11 else 0 for i, m in enumerate(sq)]
+    run(sq, sk, H=2, Hkv=1, D=256, seed=7, q_std=4.0)
+    run([s // 2 + 9 for s in sq], [max(0, k - 30) for k in sk], H=4, Hkv=1, D=192, dtype="f16", seed=8)
