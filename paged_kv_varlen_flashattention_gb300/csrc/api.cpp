@@ -868,17 +868,19 @@ SplitPlan plan_splitkv(const Args& a, bool prefill_takes_long_rows, int prefill_
     return pl;
 }
 
-// Whether longer rows go to the 8-bit prefill kernel.  A call of few row tiles (one wave of them at two
-// CTAs an SM, from its sizes) and at most 1,024 keys stays with the split-KV kernel alone: one launch, and
-// on the device, 32 / 8 heads of 128, 18.8 to 15.5 us for 64 tokens, 23.0 to 19.3 for 256, 18.9 to 17.2
-// for four times 64; past either limit the prefill kernel is ahead (four times 256: 23.9 against 58.1;
-// 256 tokens over 4,256 keys: 80.5 against 95.7).  PA_Q8_ROW_TILES=0, read per call, switches this off.
+// Whether longer rows go to the 8-bit prefill kernels.  A call of few row tiles (from its sizes: one wave at
+// two CTAs an SM, at one beyond head_dim 128) and at most 512 keys stays with the split-KV kernel alone: one
+// launch, and on the device, 32 / 8 heads of 128, 18.8 to 15.5 us for 64 tokens, 23.0 to 19.3 for 256, 27.3 to
+// 24.0 for four times 64 over 464 keys; of 256, 16.8 to 8.5 for 64 tokens and 23.3 to 19.7 for twice 64 over
+// 464.  Past either limit the prefill kernels are ahead (128: four times 256 tokens 23.9 against 58.1, twice
+// 64 over 964 keys 33.8 against 45.5; 256: four times 64 over 464 23.7 against 37.5).  PA_Q8_ROW_TILES=0, read
+// per call, switches this off.
 bool prefill_q8_wanted(const Args& a, int num_sms) {
     if (!prefill_q8_supported(a)) return false;
     const char* env = std::getenv("PA_Q8_ROW_TILES");
     if (env && env[0] == '0') return true;
     const int64_t row_tiles = ((int64_t)a.max_sq * (a.H / a.Hkv) + 31) / 32;
-    return a.max_sk > 1024 || (int64_t)a.batch * a.Hkv * row_tiles > 2 * num_sms;
+    return a.max_sk > 512 || (int64_t)a.batch * a.Hkv * row_tiles > (a.D <= 128 ? 2 : 1) * num_sms;
 }
 
 SplitPlan plan_q8(const Args& a, bool prefill_takes_long_rows, int prefill_sms, int num_sms) {

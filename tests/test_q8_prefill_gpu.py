@@ -168,7 +168,7 @@ def test_small_calls_on_row_tiles(alibi, dtype, monkeypatch):
     divide a tile, and the first sizes past the rule."""
     monkeypatch.delenv("PA_Q8_ROW_TILES")
     slopes = torch.exp2(-torch.arange(1, 11).float()) if alibi else None
-    for sq, sk in ([64], [64]), ([256], [300]), ([33, 1, 7], [1000, 1024, 0]), ([100], [1025]), ([400, 90], [400, 900]):
+    for sq, sk in ([64], [64]), ([256], [300]), ([33, 1, 7], [500, 512, 0]), ([100], [513]), ([400, 90], [400, 900]):
         run(sq, sk, H=10, Hkv=2, D=96, P=96, dtype=dtype, slopes=slopes, seed=sum(sq))
 
 
