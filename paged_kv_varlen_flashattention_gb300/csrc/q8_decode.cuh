@@ -388,9 +388,6 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
     uint64_t* v_full = k_empty + STAGES;
     uint64_t* v_empty = v_full + STAGES;
     volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG);
-    q8_row_bounds(p, tv, rows, hk, M);
-    __syncthreads();  // rows, and for a CTA's first unit the barriers
-
     if (warp >= NW) {
         int* ids = reinterpret_cast<int*>(smem + C::OFF_IDS);
         if (warp == NW)
@@ -401,6 +398,7 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
         if (p.cluster > 1) q8_cluster_passive();
         return true;
     }
+    q8_row_bounds(p, tv, rows, hk, M);
     const int rg = warp / C::KW, kq = warp % C::KW;
     constexpr int BPT = C::KPW / 32;  // blocks of 32 keys of this warp's slice of a tile
     static_assert(C::KPW % 32 == 0 && C::CK == 2, "a block is two chunks");
@@ -838,9 +836,6 @@ __device__ __forceinline__ bool decode_q8_few_rows(const CUtensorMap& tm_k, cons
     uint64_t* v_full = k_empty + STAGES;
     uint64_t* v_empty = v_full + STAGES;
     volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG);
-    q8_row_bounds(p, tv, rows, hk, 16);
-    __syncthreads();  // rows, and for a CTA's first unit the barriers
-
     if (warp >= NW) {
         int* ids = reinterpret_cast<int*>(smem + C::OFF_IDS);
         if (warp == NW)
@@ -851,6 +846,7 @@ __device__ __forceinline__ bool decode_q8_few_rows(const CUtensorMap& tm_k, cons
         if (p.cluster > 1) q8_cluster_passive();
         return true;
     }
+    q8_row_bounds(p, tv, rows, hk, 16);
     auto block_key = [&](int n) { return kbeg + n * NT + warp * 32; };  // 32 aligned keys lie in one page
     Q8Scales scales;
     scales.fetch(p, b, hk, tv.sk, 0, n_iter, block_key);
@@ -1168,9 +1164,6 @@ __device__ __forceinline__ bool decode_q8_swapped(const CUtensorMap& tm_k, const
     uint64_t* v_full = k_empty + STAGES;
     uint64_t* v_empty = v_full + STAGES;
     volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(smem + C::OFF_FLAG);
-    q8_row_bounds(p, tv, rows, hk, 16);
-    __syncthreads();  // rows, and for a CTA's first unit the barriers
-
     if (warp >= NW) {
         int* ids = reinterpret_cast<int*>(smem + C::OFF_IDS);
         if (warp == NW)
@@ -1181,6 +1174,7 @@ __device__ __forceinline__ bool decode_q8_swapped(const CUtensorMap& tm_k, const
         if (p.cluster > 1) q8_cluster_passive();
         return true;
     }
+    q8_row_bounds(p, tv, rows, hk, 16);
     auto block_key = [&](int n) { return kbeg + n * NT + warp * 32; };  // 32 aligned keys lie in one page
     Q8Scales scales;
     scales.fetch(p, b, hk, tv.sk, 0, n_iter, block_key);
@@ -1457,6 +1451,7 @@ __global__ void __launch_bounds__(NW * 32 + 64, 2)
         *abort_flag = 0u;
         fence_mbar_init();
     }
+    __syncthreads();
     // A sequence of few rows runs on the body for them, and in a kernel for two row groups one of at
     // most 16 rows on the one-group body.
     auto run_unit = [&](int b, int hk, int rt, int split, int g0, int& n_done) -> bool {
@@ -1564,6 +1559,7 @@ __global__ void __launch_bounds__(Q8WideCfg<DP_, MG>::THREADS, Q8WideCfg<DP_, MG
         *abort_flag = 0u;
         fence_mbar_init();
     }
+    __syncthreads();
     __shared__ int rank_len[kRankInCta];
     __shared__ int rank_pick;
     const int b = q8_sequence(p, rank_len, &rank_pick);
@@ -1577,8 +1573,6 @@ __global__ void __launch_bounds__(Q8WideCfg<DP_, MG>::THREADS, Q8WideCfg<DP_, MG
     const int kbeg = tv.kt0 + t_begin * NT;
     const Q8Rows rows = q8_rows(smem + C::OFF_ROW, M);
     float* xmax = reinterpret_cast<float*>(smem + C::OFF_MAX);
-    q8_row_bounds(p, tv, rows, hk, M);
-    __syncthreads();
     if (warp >= NW) {
         int* ids = reinterpret_cast<int*>(smem + C::OFF_IDS);
         if (warp == NW)
@@ -1588,6 +1582,7 @@ __global__ void __launch_bounds__(Q8WideCfg<DP_, MG>::THREADS, Q8WideCfg<DP_, MG
                                        kbeg, n_iter, 0, abort_flag);
         return;
     }
+    q8_row_bounds(p, tv, rows, hk, M);
     const int rg = warp / C::KS, slice = warp % C::KS;
     auto block_key = [&](int n) { return kbeg + n * NT + slice * NB * 8; };
     Q8Scales scales;
