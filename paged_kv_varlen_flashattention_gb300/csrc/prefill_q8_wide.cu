@@ -3,22 +3,24 @@
 // The mathematics of prefill_q8.cu (q in e4m3 terms against K as it is in the cache, P.V on f16 with V
 // converted in the CTA, the page's scales in the softmax) for rows whose accumulator takes half of the
 // tensor memory: an item is one 128-row query tile of one (sequence, kv head), key tiles have 64 keys, and S
-// has two buffers, so that the products of S(j + 1) and S(j + 2) run beside the softmax of tile j. A thread
-// of the softmax holds its row's 64 scores in registers.
+// has four buffers, so that its products run up to three tiles ahead of the softmax. A thread of the softmax
+// holds its row's 64 scores in registers.
 //
 // Roles (512 threads, four warpgroups):
 //   warp 0      takes items and publishes them; K tiles and their scales
-//   warp 1      MMA issuer: S(0), S(1), then P.V(j), S(j + 2)
+//   warp 1      MMA issuer: S(0), S(1), S(2), then S(j + 3), P.V(j)
 //   warp 2      V tiles
 //   warps 4..7  softmax, a row (TMEM lane) a thread
 //   warps 8..15 converters: q into its terms at the start of an item, then V tile by tile
 //
 // Tensor-core bound: 4 D flops per (row, key) at the f16 rate (f16 q: 5 D).
-// Two prompts of 4,096 tokens, 32 / 8 heads: 514 us at head_dim 256 in bf16 (1.07 PFLOP/s, 0.56 of the
-// measured bf16 rate), 624 in f16; the same on row tiles of the split-KV kernel takes 2,965 and 2,915.
-// What bounds it is the step: S(j), its softmax and P.V(j) each wait for the one before, and the other
-// buffer's products fill only part of the softmax. Columns past the head dim are computed on zeros
-// (head_dim 192 takes what 256 does).
+// Two prompts of 4,096 tokens, 32 / 8 heads: 521 us at head_dim 256 in bf16 (1.05 PFLOP/s, 0.55 of the
+// measured bf16 rate), 580 in f16; the same on row tiles of the split-KV kernel takes 2,965 and 2,915, and
+// with two buffers of S 512 and 623. The tensor pipe is active 46 % of the time. What bounds it is the
+// softmax: one warp a scheduler takes 1.2 us for its 32 rows of 64 keys, most of it waiting (tensor
+// memory, dependent instructions), not issuing. A K ring of three or two stages with the V ring at
+// three or four is 2 and 3 % slower. Columns past the head dim are computed on zeros (head_dim 192 takes what
+// 256 does).
 #include <algorithm>
 #include <cfloat>
 #include <cstdio>
@@ -40,7 +42,7 @@ constexpr float kPwOffset = 7.f;
 
 template <int NTERM>
 struct PwCfg {
-    static constexpr int DP = 256, NT = 64;
+    static constexpr int DP = 256, NT = 64, NS = 4;  // NS: buffers of S
     static constexpr int QTILE = 128 * 128;  // 128 rows of 64 columns of q as loaded, or of 128 columns of a term
     static constexpr int CHUNK = NT * 128;   // 64 keys of 128 columns of codes, or of 64 columns of V in f16
     static constexpr int KS = NTERM == 2 ? 4 : 2, VR = 2;
@@ -52,18 +54,18 @@ struct PwCfg {
     static constexpr int OFF_VC = OFF_VR + VR * TILE;
     static constexpr int OFF_BAR = OFF_VC + 2 * VC_TILE;
     // q_raw, q_full, q_free, k_full[KS], k_empty[KS], vr_full[VR], vr_empty[VR], vc_full[2], vc_empty[2],
-    // s_full[2], pv_done[2], p_full[2], drain, item_ready[2], item_free[2]
-    static constexpr int NBAR = 3 + 2 * KS + 2 * VR + 10 + 1 + 4;
+    // s_full[4], pv_done[4], p_full[4], drain, item_ready[2], item_free[2]
+    static constexpr int NBAR = 3 + 2 * KS + 2 * VR + 4 + 3 * NS + 1 + 4;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;  // tmem base, abort flag
     static constexpr int OFF_SLOT = OFF_MISC + 16;       // two item slots
     static constexpr int SC_RING = 8;
     static constexpr int OFF_SC = OFF_SLOT + 128;          // [tile % 8]: ks[2], log2 vs[2], 1 / vs[2]
     static constexpr int OFF_EXP = OFF_SC + SC_RING * 32;  // [item parity][row]: e of the row, int8
     static constexpr int SMEM = OFF_EXP + 256 + 1024;
-    static constexpr uint32_t T_S = 0, T_O = 256;  // two buffers of S, 64 columns each; O
+    static constexpr uint32_t T_S = 0, T_O = 256;  // the buffers of S, 64 columns each; O
     // The scale ring: the K producer writes position g after S(g - KS) has completed, which follows P.V of
-    // g - KS - 2 and so that tile's softmax; what is overwritten (g - 8) has been read.
-    static_assert(KS + 2 <= SC_RING, "scale ring");
+    // g - KS - NS and so that tile's softmax; what is overwritten (g - 8) has been read.
+    static_assert(KS + NS <= SC_RING, "scale ring");
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                            const __grid_constant__ CUtensorMap tm_v, const PrefillQ8Params p) {
     constexpr int NTERM = std::is_same<T, __half>::value ? 3 : 2;
     using C = PwCfg<NTERM>;
-    constexpr int KS = C::KS, VR = C::VR, DP = C::DP, NT = C::NT;
+    constexpr int KS = C::KS, VR = C::VR, DP = C::DP, NT = C::NT, NS = C::NS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -109,9 +111,9 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     uint64_t* vc_full = vr_empty + VR;
     uint64_t* vc_empty = vc_full + 2;
     uint64_t* s_full = vc_empty + 2;  // [buffer]
-    uint64_t* pv_done = s_full + 2;   // [buffer]
-    uint64_t* p_full = pv_done + 2;   // [buffer]: a softmax warp can be a tile ahead of another
-    uint64_t* drain = p_full + 2;
+    uint64_t* pv_done = s_full + NS;  // [buffer]
+    uint64_t* p_full = pv_done + NS;  // [buffer]: a softmax warp can be NS - 1 tiles ahead of another
+    uint64_t* drain = p_full + NS;
     uint64_t* item_ready = drain + 1;      // [slot]
     uint64_t* item_free = item_ready + 2;  // [slot]
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
@@ -131,12 +133,14 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             mbar_init(&vr_full[s], 1);
             mbar_init(&vr_empty[s], kPwConverters);
         }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(&vc_full[x], kPwConverters);
-            mbar_init(&vc_empty[x], 1);
+        for (int x = 0; x < NS; ++x) {
             mbar_init(&s_full[x], 1);
             mbar_init(&pv_done[x], 1);
             mbar_init(&p_full[x], 4);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&vc_full[x], kPwConverters);
+            mbar_init(&vc_empty[x], 1);
             mbar_init(&item_ready[x], 1);
             mbar_init(&item_free[x], 6 + kPwConverters);  // the V producer, the issuer, four softmax warps, the converters
         }
@@ -314,11 +318,11 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             for (int t = 0; t < NTERM; ++t)
 #pragma unroll
                 for (int kk = 0; kk < DP / 32; ++kk)
-                    tc::mma_f8_ss_elect(tmem + C::T_S + (g & 1) * NT,
+                    tc::mma_f8_ss_elect(tmem + C::T_S + g % NS * NT,
                                         da + (uint64_t)((t * 2 + kk / 4) * (C::QTILE >> 4) + (kk & 3) * 2),
                                         db + (uint64_t)((kk / 4) * (C::CHUNK >> 4) + (kk & 3) * 2), IDESC_S,
                                         t + kk > 0 ? 1u : 0u);
-            tc::commit_elect(&s_full[g & 1]);
+            tc::commit_elect(&s_full[g % NS]);
             tc::commit_elect(&k_empty[g % KS]);
             if (last) tc::commit_elect(q_free);
             __syncwarp();
@@ -330,23 +334,22 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             if (it.bad || it.n_tiles == 0) continue;
             const int n = it.n_tiles;
             if (!(ok = wait_all(q_full, lq & 1))) break;
-            // S(g) takes the buffer of P(g - 2), whose P.V has been issued before it
-            if (!(ok = issue_s(g0, n == 1))) break;
-            if (n > 1 && !(ok = issue_s(g0 + 1, n == 2))) break;
+            // S(g) takes the buffer of P(g - NS), whose P.V has been issued before it
+            for (int j = 0; ok && j < min(n, NS - 1); ++j) ok = issue_s(g0 + j, j + 1 == n);
             for (int j = 0; ok && j < n; ++j) {
                 const int g = g0 + j;
+                if (j + NS - 1 < n && !(ok = issue_s(g + NS - 1, j + NS == n))) break;
                 if (!(ok = wait_all(&vc_full[g & 1], (g >> 1) & 1))) break;
-                if (!(ok = wait_all(&p_full[g & 1], (g >> 1) & 1))) break;
+                if (!(ok = wait_all(&p_full[g % NS], (g / NS) & 1))) break;
                 const uint64_t db = dv0 + (uint64_t)((g & 1) * (C::VC_TILE >> 4));
                 const uint32_t first = j > 0 ? 1u : 0u;
 #pragma unroll
                 for (int kk = 0; kk < NT / 16; ++kk)
-                    tc::mma_ts_elect(d_o, tmem + C::T_S + (g & 1) * NT + kk * 8, db + (uint64_t)(kk * (2048 / 16)), IDESC_O,
+                    tc::mma_ts_elect(d_o, tmem + C::T_S + g % NS * NT + kk * 8, db + (uint64_t)(kk * (2048 / 16)), IDESC_O,
                                      kk > 0 ? 1u : first);
                 tc::commit_elect(&vc_empty[g & 1]);
-                tc::commit_elect(&pv_done[g & 1]);
+                tc::commit_elect(&pv_done[g % NS]);
                 __syncwarp();
-                if (j + 2 < n) ok = issue_s(g + 2, j + 3 == n);
             }
             g0 += n;
             ++lq;
@@ -489,10 +492,10 @@ __global__ void __launch_bounds__(kPwThreads, 1)
         const bool pad = row >= trows;
         int g0 = 0, ld = 0;
         bool ok = true;
-        // P.V of tile g, one of the two last whose P was given (so its barrier can be at most one phase on;
-        // nor is it one behind, for S(g + 1) has been seen, or P.V of g - 2 precedes S(g), which has).
+        // P.V of tile g, the last whose P was given. Its barrier is not a phase on (P.V of g + NS is not issued
+        // yet) nor one behind (P.V of g - NS precedes S(g), which has been seen).
         auto wait_pv = [&](int g) {
-            return __all_sync(0xffffffffu, wait_bar(&pv_done[g & 1], (g >> 1) & 1, abort_flag, p.err, p.wait_ns));
+            return __all_sync(0xffffffffu, wait_bar(&pv_done[g % NS], (g / NS) & 1, abort_flag, p.err, p.wait_ns));
         };
         for (int k = 0; ok; ++k) {
             PfItem it;
@@ -522,8 +525,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
             // One key tile: S -> running reference -> (rare) O rescale -> P.
             auto step = [&](int j) -> bool {
                 const int g = g0 + j, kt = tile_key(it, j);
-                const uint32_t s_addr = tmem + lane_addr + C::T_S + (g & 1) * NT;
-                if (!__all_sync(0xffffffffu, wait_bar(&s_full[g & 1], (g >> 1) & 1, abort_flag, p.err, p.wait_ns))) return false;
+                const uint32_t s_addr = tmem + lane_addr + C::T_S + g % NS * NT;
+                if (!__all_sync(0xffffffffu, wait_bar(&s_full[g % NS], (g / NS) & 1, abort_flag, p.err, p.wait_ns))) return false;
                 tc::fence_after_sync();
                 const float* slot = sc_ring + (g % C::SC_RING) * 8;
                 if (j == 0) sl = p.scale_log2 * __int_as_float((127 - row_exp[(ld & 1) * 128 + row]) << 23);
@@ -611,7 +614,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                 tc::wait_st();
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full[g & 1]);
+                if (lane == 0) mbar_arrive(&p_full[g % NS]);
                 return true;
             };
 #pragma unroll 1
