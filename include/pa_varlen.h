@@ -363,10 +363,12 @@ int pa_kv_append_q8_check(const pa_tensor* q, const pa_tensor* k_new, const pa_t
  *                V scales below 2^-100 (and zero) are read as 2^-100
  *  alibi_slopes  (num_heads,) f32 or NULL
  *  the rest      as for pa_varlen_fwd
- * Scores are accumulated in fp32 from exact codes; the softmax weights are rounded to f16 (11
- * bits) for the product with V, whatever q's type.  A code that is NaN, or a scale that is
- * NaN, reaches the rows that attend its key; one that no row of a call's tile attends (past the
- * sequence, before every window) does not matter.
+ * Scores, sums and the output are accumulated in fp32 from exact codes.  An element of q counts to
+ * within 2^-9 (bf16; f16: 2^-13) of itself or 2^-17 of its row's largest, or better; the softmax
+ * weights are rounded for the product with V to 2^-9 of themselves in bf16 calls, 2^-11 in f16
+ * calls, or better.  A code that is
+ * NaN reaches the rows that attend its key; a code, or a scale, of keys that no row of a call's tile
+ * attends (past the sequence, before every window) does not matter.
  * Host checks: those of pa_varlen_fwd (the caches' dtype aside), then the caches' dtype, the
  * scales, head_dim and strides as for pa_kv_append_q8; PA_ERR_UNSUPPORTED when max_seqlen_k needs
  * more than 1024 splits of 8192 keys.  Scratch, streams, graph capture and threads as for

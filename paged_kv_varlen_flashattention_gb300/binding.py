@@ -10,7 +10,6 @@ from __future__ import annotations
 import ctypes
 import math
 import os
-import struct
 from typing import Optional, Tuple
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -85,7 +84,7 @@ def load():
         lib.pa_kv_append.argtypes = [_TP] * 7 + [ctypes.c_int32, ctypes.c_void_p]
         lib.pa_kv_append_check.restype = ctypes.c_int
         lib.pa_kv_append_check.argtypes = [_TP] * 7 + [ctypes.c_int32]
-        # descriptors as addresses: these calls take them packed (see _pack) or by reference
+        # descriptors as addresses: these calls take them packed in one buffer (tensor_args.cpp) or by reference
         _VP = ctypes.c_void_p
         _ROPE = [_VP] * 5 + [ctypes.c_int32] + [_VP] * 5 + [ctypes.c_int32, _VP]
         lib.pa_kv_append_rope.restype = ctypes.c_int
@@ -146,11 +145,8 @@ def describe(t) -> Optional[PaTensor]:
     return PaTensor(t.data_ptr(), _dtype_code(t), n, _I64x4(*shape), _I64x4(*stride))
 
 
-# pa_tensor by rank: data, dtype, ndim, shape[4], stride[4] with zeros behind the rank
-_PACK = [None] + [struct.Struct(f"Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x").pack_into for n in (1, 2, 3, 4)]
-
-
-_runtime = None  # (torch, current device, raw current stream of a device), bound at the first call
+# (torch, current device, raw current stream of a device, the module that reads tensors), bound at the first call
+_runtime = None
 
 
 def _bind_runtime():
@@ -162,37 +158,22 @@ def _bind_runtime():
     raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw_stream is None:
         raw_stream = lambda index: torch.cuda.current_stream(index).cuda_stream  # noqa: E731
-    _runtime = (torch, current_device, raw_stream)
+    from importlib import util
+    from .build import tensor_args_path
+    path = tensor_args_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} not built for this torch; run: python -c 'import __graft_entry__ as g; g.build()'")
+    spec = util.spec_from_file_location("_pa_tensor_args", path)
+    tensor_args = util.module_from_spec(spec)
+    spec.loader.exec_module(tensor_args)
+    _runtime = (torch, current_device, raw_stream, tensor_args)
     return _runtime
-
-
-def _pack(tensors):
-    """(buffer, addresses) of the tensors' descriptors in one buffer that the caller keeps
-    alive over the call; None stays None.  About a third of the host time of one ctypes
-    structure per tensor."""
-    code = _DTYPE_CODES.get
-    buf = bytearray(80 * len(tensors))
-    at = ctypes.addressof(ctypes.c_char.from_buffer(buf))
-    where, off = [], 0
-    for t in tensors:
-        if t is None:
-            where.append(None)
-        else:
-            shape = t.shape
-            n = len(shape)
-            if 1 <= n <= 4:
-                _PACK[n](buf, off, t.data_ptr(), code(t.dtype, -1), n, *shape, *t.stride())
-            else:  # no rank the library takes: the rank alone, for its refusal
-                _PACK[1](buf, off, t.data_ptr(), code(t.dtype, -1), n, 0, 1)
-            where.append(at + off)
-        off += 80
-    return buf, where
 
 
 def _call(fn, on, stream, *args) -> None:
     """fn(*args, stream) with the device of tensor ``on`` current (its current stream when
     ``stream`` is None); raises PaError on a non-zero status."""
-    torch, current_device, raw_stream = _runtime
+    torch, current_device, raw_stream, _ = _runtime
     index = on.get_device()
     if index < 0:  # no CUDA tensor: the library refuses it
         rc = fn(*args, None)
@@ -342,11 +323,11 @@ def kv_append_rope(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_ca
     the tokens' positions with the tables ``cos`` / ``sin`` (max_position, rot / 2) fp32,
     and writes k and v into their pages, in place.  Returns the rotated q (``q_out``,
     allocated with torch when not given; pass ``q`` itself to rotate in place) or None."""
-    torch = (_runtime or _bind_runtime())[0]
+    tensors = (_runtime or _bind_runtime())[3]
     P = page_block_size if page_block_size is not None else k_cache.shape[1]
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    keep, ds = _pack((q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, q_out))
+        q_out = tensors.empty_like(q)
+    keep, *ds = tensors.pack(q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, q_out)
     _call(_lib.pa_kv_append_rope, k_new, stream, *ds[:5], 1 if interleaved else 0, *ds[5:10], int(P), ds[10])
     return q_out
 
@@ -364,12 +345,12 @@ def kv_append_q8(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_cach
     ``torch.float8_e4m3fn`` codes with the fp32 scales ``k_scale`` / ``v_scale``
     (num_blocks, num_heads_k) of every page and kv head, updated in place.  Without ``cos`` and
     ``sin`` the keys are held as they are (and ``q`` must not be given)."""
-    torch = (_runtime or _bind_runtime())[0]
+    tensors = (_runtime or _bind_runtime())[3]
     P = page_block_size if page_block_size is not None else k_cache.shape[1]
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    keep, ds = _pack((q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, k_scale,
-                      v_scale, q_out))
+        q_out = tensors.empty_like(q)
+    keep, *ds = tensors.pack(q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, k_scale, v_scale,
+                              q_out)
     _call(_lib.pa_kv_append_q8, k_new, stream, *ds[:5], 1 if interleaved else 0, *ds[5:12], int(P), ds[12])
     return q_out
 
@@ -388,18 +369,18 @@ def varlen_fwd_q8(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlen
     ``torch.float8_e4m3fn`` codes with the fp32 scales ``k_scale`` / ``v_scale`` (num_blocks,
     num_heads_k) of every page and kv head; q and out are f16 or bf16.  Returns (out,
     softmax_lse), allocated with torch when not given."""
-    torch = (_runtime or _bind_runtime())[0]
+    tensors = (_runtime or _bind_runtime())[3]
     if max_seqlen_q is None or max_seqlen_k is None:
         raise ValueError("max_seqlen_q and max_seqlen_k are required")
-    shape, device, cache = q.shape, q.device, k_cache.shape
+    shape, cache = q.shape, k_cache.shape
     if softmax_scale is None:
         softmax_scale = shape[-1] ** -0.5
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=device)
+        out = tensors.empty_like(q)
     if softmax_lse is None:
-        softmax_lse = torch.empty((shape[1], shape[0]), dtype=torch.float32, device=device)
-    keep, ds = _pack((q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_table, alibi_slopes, out,
-                      softmax_lse))
+        softmax_lse = tensors.empty_lse(q)
+    keep, *ds = tensors.pack(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_table, alibi_slopes, out,
+                              softmax_lse)
     _call(_lib.pa_varlen_fwd_q8, q, stream, *ds[:8], int(max_seqlen_q), int(max_seqlen_k), shape[-2], cache[-2],
           shape[-1], int(page_block_size) if page_block_size is not None else cache[1], softmax_scale, window_left,
           window_right, *ds[8:])

@@ -1,11 +1,13 @@
 """Builds libpa_varlen.so in-tree with nvcc for sm_103a (one -gencode, translation
-units compiled in parallel, then linked with the static CUDA runtime)."""
+units compiled in parallel, then linked with the static CUDA runtime), and beside it the
+binding's CPython module, which reads tensors of the installed torch."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +22,27 @@ SOURCES = ["api.cpp", "errword.cu", "splitkv_bf16.cu", "splitkv_f16.cu", "prefil
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
+def tensor_args_path() -> str:
+    """The binding's module, built for one version of torch and of Python."""
+    import torch
+    return os.path.join(PKG, f"_pa_tensor_args-{torch.__version__}-{sysconfig.get_config_var('SOABI')}.so")
+
+
+def build_tensor_args(path: str) -> None:
+    import torch
+    home = os.path.dirname(torch.__file__)
+    tmp = path + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(home, "include"),
+           os.path.join(CSRC, "tensor_args.cpp"), "-o", tmp, "-L", os.path.join(home, "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on tensor_args.cpp:\n{r.stderr[-6000:]}")
+    os.replace(tmp, path)
+
+
 def nvcc() -> str:
     cand = os.environ.get("NVCC") or shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc"
     return cand
@@ -30,9 +53,9 @@ def _flags():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(tensor_args_path()):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(tensor_args_path()))
     for d in (CSRC, INCLUDE):
         for f in os.listdir(d):
             if os.path.getmtime(os.path.join(d, f)) > t:
@@ -56,7 +79,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
+        module = ex.submit(build_tensor_args, tensor_args_path())
         objs = list(ex.map(compile_one, SOURCES))
+        module.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)

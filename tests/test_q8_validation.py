@@ -201,3 +201,27 @@ def test_plain_attention_is_torchs():
                                                              scale=0.3)
         assert torch.allclose(out[at:at + n].permute(1, 0, 2), o, atol=1e-12)
         at += n
+
+
+def test_tensors_as_descriptors():
+    """The binding's module: address, type, sizes and strides of views, None, ranks and types without a code, and
+    the outputs it allocates."""
+    import torch
+    binding._bind_runtime()
+    m = binding._runtime[3]
+    x = torch.zeros(3, 4, 8, dtype=torch.bfloat16)[1:, ::2]
+    types = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.int32: 3, torch.float8_e4m3fn: 4, torch.int64: -1}
+    buf, *at = m.pack(x, None, *[torch.empty(2, 3, dtype=t) for t in types], torch.zeros(1, 1, 1, 1, 1))
+    d = [a if a is None else binding.PaTensor.from_address(a) for a in at]
+    assert (d[0].data, d[0].dtype, d[0].ndim) == (x.data_ptr(), 1, 3)
+    assert list(d[0].shape) == [2, 2, 8, 0] and list(d[0].stride) == [32, 16, 1, 0]
+    assert d[1] is None and [e.dtype for e in d[2:8]] == list(types.values()) and d[8].ndim == 5
+    assert len(buf) == 80 * len(d)
+    out, lse = m.empty_like(x), m.empty_lse(x)
+    assert out.shape == x.shape and out.is_contiguous() and out.dtype == x.dtype
+    assert lse.shape == (2, 2) and lse.dtype == torch.float32 and m.empty_lse(torch.empty(3)).numel() == 0
+    for f in (m.pack, m.empty_like, m.empty_lse):
+        with pytest.raises(TypeError):
+            f(3)
+    with pytest.raises(RuntimeError):
+        m.pack(torch.zeros(2, 2).to_sparse())
