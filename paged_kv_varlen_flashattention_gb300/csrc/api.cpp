@@ -900,11 +900,14 @@ SplitPlan plan_q8(const Args& a, bool prefill_takes_long_rows, int prefill_sms, 
     const int64_t tiles_max = std::max<int64_t>(1, kspan / pl.nt + 2);
     const int64_t units = (int64_t)a.batch * a.Hkv * pl.row_tiles;
     pl.slots = num_sms * (a.dtype == PA_BF16 ? q8_occupancy_bf16(pl) : q8_occupancy_f16(pl));
-    // As the 16-bit plan: one wave of splits when there are fewer units than resident CTAs, one
-    // CTA per unit otherwise or beside a prefill grid that may take every SM; a split takes at
-    // least 256 keys and 16 per row (its fp32 partial, written and read, is then at most a
-    // quarter of the K/V bytes), and never more than the block ids and scales a CTA stages.
-    const int64_t slots = prefill_sms >= num_sms ? 0 : pl.slots;
+    // One wave of splits when there are fewer units than resident CTAs on the SMs that a prefill grid
+    // beside this one leaves, one CTA per unit otherwise; a split takes at least 256 keys and 16
+    // per row (its fp32 partial, written and read, is then at most a quarter of the K/V bytes), and
+    // never more than the block ids and scales a CTA stages.  (Beside a 256-token chunk over 1,256 keys, 8
+    // sequences of 2,000 keys, 32 / 8 heads, take 33.8 us in all, with splits for every SM 55.0: CTAs of
+    // a cluster start together, and the ones too many wait for the prefill to end.  Where the decode
+    // part is by far the longer the splits would win: of 16,000 keys 104.3 against 92.6.)
+    const int64_t slots = (int64_t)pl.slots * std::max(0, num_sms - prefill_sms) / num_sms;
     int64_t splits = units < slots ? slots / units : 1;
     splits = std::max<int64_t>(1, std::min(splits, tiles_max));
     const int64_t min_tiles = std::max<int64_t>(256, 16ll * pl.tile_rows) / pl.nt;
@@ -931,7 +934,7 @@ SplitPlan plan_q8(const Args& a, bool prefill_takes_long_rows, int prefill_sms, 
     }
     pl.work = pl.row_tiles == 1 && pl.dp <= 128 && a.batch >= kWorkMinBatch && a.batch <= kMaxOrderBatch &&
               pl.max_splits > 1;
-    const bool one_wave = units * pl.max_splits * pl.cluster <= pl.slots;
+    const bool one_wave = units * pl.max_splits * pl.cluster <= slots;
     const bool ranked = !pl.work && !one_wave;
     pl.rank_in_cta = ranked && a.batch >= 2 && a.batch <= kRankInCta;
     pl.order_bytes = ranked && a.batch > kRankInCta && a.batch <= kMaxOrderBatch
@@ -992,7 +995,10 @@ int launch_forward(pa::Args& a, void* stream, ScratchFn scratch, void* scratch_c
     // SMs the persistent prefill grid may hold beside the decode-class pass (it runs before
     // that pass, not beside it, when there is no side stream)
     const int prefill_sms =
-        use_prefill && side_stream_ok ? (int)std::min<int64_t>(sm_count(), pa::prefill_items_bound(a)) : 0;
+        use_prefill && side_stream_ok
+            ? (int)std::min<int64_t>(sm_count(), a.k_scale ? pa::prefill_q8_items_bound(a, sm_count())
+                                                           : pa::prefill_items_bound(a))
+            : 0;
     const pa::SplitPlan plan = a.k_scale ? pa::plan_q8(a, use_prefill, prefill_sms, sm_count())
                                          : pa::plan_splitkv(a, use_prefill, prefill_sms, sm_count());
     if (plan.max_splits > 1024)  // only an 8-bit call's: its splits are bounded, and so is the combine

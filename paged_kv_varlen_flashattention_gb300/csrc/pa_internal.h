@@ -100,6 +100,7 @@ constexpr size_t kPrefillCounterBytes = 256;
 int launch_prefill(const Args& a, int* counter, unsigned int* err, char* msg, size_t msg_len);
 // The same over an 8-bit cache (prefill_q8.cu).
 bool prefill_q8_supported(const Args& a);
+int64_t prefill_q8_items_bound(const Args& a, int num_sms);
 int launch_prefill_q8_wide(const Args& a, int* counter, unsigned int* err, char* msg, size_t msg_len);
 int launch_prefill_q8(const Args& a, int* counter, unsigned int* err, char* msg, size_t msg_len);
 // Upper bound of the prefill kernel's work items (its grid is min(SMs, items)).

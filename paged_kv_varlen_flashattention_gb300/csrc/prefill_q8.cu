@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kPqThreads, 1)
         // ---------------- item taker, K producer ----------------
         // Items as in prefill_kernel: w = pair * Hkv + kv head, each sequence's last pair first.
         const int total = p.pairs * p.Hkv;
+        const int per = p.single ? qpt : 2 * qpt;  // queries of an item
         if (!p.withhold) prefetch_tmap(&tm_k);
         int w_next = lane == 0 ? atomicAdd(p.counter, 1) : 0;
         int gk = 0;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                     int pairs = 0;
                     if (bb < p.batch) {
                         const int sqb = p.cu_q[bb + 1] - p.cu_q[bb];
-                        pairs = (int64_t)sqb * p.G > p.rows_cap ? (sqb + 2 * qpt - 1) / (2 * qpt) : 0;
+                        pairs = (int64_t)sqb * p.G > p.rows_cap ? (sqb + per - 1) / per : 0;
                     }
                     int incl = pairs;
 #pragma unroll
@@ -257,7 +258,12 @@ __global__ void __launch_bounds__(kPqThreads, 1)
                         remaining -= __shfl_sync(0xffffffffu, incl, 31);
                     }
                 }
-                if (it.b >= 0) pf_item(p, qpt, it);
+                if (it.b >= 0) {
+                    if (p.single)
+                        pf_single_item<128>(p, qpt, it);
+                    else
+                        pf_item(p, qpt, it);
+                }
             }
             if (it.b >= 0 && lane == 0) w_next = atomicAdd(p.counter, 1);
             if (k >= 2 && !wait_all(&item_free[k & 1], ((k >> 1) - 1) & 1)) break;
@@ -735,11 +741,9 @@ int run_prefill_q8(const Args& a, const PrefillQ8Params& pp, char* msg, size_t m
     constexpr int SMEM = PqCfg<DP, std::is_same<T, __half>::value ? 3 : 2>::SMEM;
     auto kern = prefill_q8_kernel<T, DP, ALIBI>;
     static std::atomic<uint64_t> configured{0};
-    int dev = 0, sms = 0;
+    const int sms = device_sms();
     cudaError_t e = set_shared_memory(kern, SMEM, configured);
-    if (e == cudaSuccess) e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) {
+    if (e != cudaSuccess || sms <= 0) {
         snprintf(msg, msg_len, "configuring the q8 prefill (%d bytes of shared memory): %s", SMEM, cudaGetErrorString(e));
         return PA_ERR_CUDA;
     }
@@ -789,13 +793,17 @@ int launch_prefill_q8_t(const Args& a, const PrefillQ8Params& pp, char* msg, siz
 // same conditions as the 16-bit kernels').
 bool prefill_q8_supported(const Args& a) { return prefill_supported(a); }
 
+int64_t prefill_q8_items_bound(const Args& a, int num_sms) {
+    return prefill_q8_single(a, num_sms) ? prefill_q8_tiles(a) * a.Hkv : prefill_items_bound(a);
+}
+
 int launch_prefill_q8(const Args& a, int* counter, unsigned int* err, char* msg, size_t msg_len) {
     if (a.D > 128) return launch_prefill_q8_wide(a, counter, err, msg, msg_len);
     if (!counter) {
         snprintf(msg, msg_len, "the prefill kernels need a device item counter");
         return PA_ERR_ARG;
     }
-    const PrefillQ8Params pp = prefill_q8_params(a, counter, err, 128);
+    const PrefillQ8Params pp = prefill_q8_params(a, counter, err, 128, device_sms());
     return a.dtype == PA_BF16 ? launch_prefill_q8_t<__nv_bfloat16>(a, pp, msg, msg_len)
                               : launch_prefill_q8_t<__half>(a, pp, msg, msg_len);
 }

@@ -69,27 +69,6 @@ struct PwCfg {
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
-// One query tile of qpt whole queries, with its 64-key tiles.
-__device__ __forceinline__ void pw_item(const PrefillParams& p, int qpt, PfItem& it) {
-    it.q0 = p.cu_q[it.b];
-    const int q1 = p.cu_q[it.b + 1];
-    it.k0 = p.cu_k[it.b];
-    const int k1 = p.cu_k[it.b + 1];
-    it.sq = q1 - it.q0;
-    it.sk = k1 - it.k0;
-    it.bad = it.sq < 0 || it.sk < 0 || it.sq > p.max_sq || it.sk > p.max_sk || it.q0 < 0 || q1 > p.total_q;
-    it.n_tiles = 0;
-    it.has_b = 0;
-    if (it.bad) return;
-    it.i0 = it.u * qpt;
-    const int i_last = min(it.sq - 1, it.i0 + qpt - 1);
-    const int64_t cdiag = (int64_t)it.sk - it.sq;
-    const int64_t lo = p.wl >= 0 ? max64(0, it.i0 + cdiag - p.wl) : 0;
-    const int64_t hi = p.wr >= 0 ? min64((int64_t)it.sk - 1, i_last + cdiag + p.wr) : (int64_t)it.sk - 1;
-    it.kt0 = hi >= lo ? (int)(lo & ~int64_t(63)) : 0;
-    it.n_tiles = hi >= lo ? (int)((hi - it.kt0) / 64 + 1) : 0;
-}
-
 template <typename T, bool ALIBI>
 __global__ void __launch_bounds__(kPwThreads, 1)
     prefill_q8_wide_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -273,7 +252,7 @@ __global__ void __launch_bounds__(kPwThreads, 1)
                         remaining -= __shfl_sync(0xffffffffu, incl, 31);
                     }
                 }
-                if (it.b >= 0) pw_item(p, qpt, it);
+                if (it.b >= 0) pf_single_item<NT>(p, qpt, it);
             }
             if (it.b >= 0 && lane == 0) w_next = atomicAdd(p.counter, 1);
             if (k >= 2 && !wait_all(&item_free[k & 1], ((k >> 1) - 1) & 1)) break;
@@ -661,11 +640,9 @@ int run_prefill_q8_wide(const Args& a, const PrefillQ8Params& pp, char* msg, siz
     constexpr int SMEM = PwCfg<std::is_same<T, __half>::value ? 3 : 2>::SMEM;
     auto kern = prefill_q8_wide_kernel<T, ALIBI>;
     static std::atomic<uint64_t> configured{0};
-    int dev = 0, sms = 0;
+    const int sms = device_sms();
     cudaError_t e = set_shared_memory(kern, SMEM, configured);
-    if (e == cudaSuccess) e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) {
+    if (e != cudaSuccess || sms <= 0) {
         snprintf(msg, msg_len, "configuring the wide q8 prefill (%d bytes of shared memory): %s", SMEM, cudaGetErrorString(e));
         return PA_ERR_CUDA;
     }
@@ -709,7 +686,7 @@ int launch_prefill_q8_wide(const Args& a, int* counter, unsigned int* err, char*
         snprintf(msg, msg_len, "the prefill kernels need a device item counter");
         return PA_ERR_ARG;
     }
-    const PrefillQ8Params pp = prefill_q8_params(a, counter, err, 64);
+    const PrefillQ8Params pp = prefill_q8_params(a, counter, err, 64, device_sms());
     if (a.dtype == PA_BF16)
         return a.alibi ? run_prefill_q8_wide<__nv_bfloat16, true>(a, pp, msg, msg_len)
                        : run_prefill_q8_wide<__nv_bfloat16, false>(a, pp, msg, msg_len);
