@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kPqThreads, 1)
         // Thread t of warp w holds row (TMEM lane) 32 (w % 4) + t with all 128 keys of a tile, so a row
         // needs no exchange, and the two warps of a scheduler, one of each tile, are at different
         // points of their steps: one's exponentials run under the other's loads and waits.  On eight
-        // prompts of 1024..8192 tokens: 1,596 us; with all eight warps on tile A and then on tile B, two
+        // prompts of 1024..8192 tokens: 1,596 us (1,546 with the later steps); with all eight warps on tile A and then on tile B, two
         // rows and 64 keys of each a thread, as in prefill_kernel, 1,793; with sixteen warps, half a row a
         // thread, 1,750.
         const int x = (warp - 4) >> 2;

@@ -26,7 +26,11 @@
 // one byte permute per register puts the two keys of a column side by side, and even and odd
 // columns go to two accumulators, whose lanes hold four consecutive columns.
 //
-// HBM-bound: 2 bytes per (key, kv head, column).
+// (That is the body for 9..32 rows; fewer rows take their terms side by side in one e4m3 product, below.)
+//
+// HBM-bound: 2 bytes per (key, kv head, column). 64 sequences of 512..4,096 keys, 32 / 8 heads of 128 in bf16 take
+// 63.4 us, 0.71 of the copy rate (4.8 TB/s); copies of the kernel without any arithmetic took 57: what is
+// not hidden is a unit's start, about 6 us of dependent reads until its first keys are there, and its merge.
 #pragma once
 
 #include "q8_common.cuh"
