@@ -31,7 +31,6 @@
 #include <algorithm>
 #include <cfloat>
 #include <cstdio>
-#include <cstdlib>
 #include <type_traits>
 
 #include "prefill_q8_common.cuh"

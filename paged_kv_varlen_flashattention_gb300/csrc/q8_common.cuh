@@ -22,7 +22,6 @@ cudaError_t set_shared_memory(K kernel, int bytes, std::atomic<uint64_t>& device
     return e;
 }
 
-constexpr float kE4m3Max = 448.f;
 constexpr int kScaleExpMin = -100;  // the smallest scale an append gives a page, and a read sees, is 2^-100
 
 // Two fp32 values rounded to e4m3 (to nearest even, beyond 448 to 448): `lo` in the low byte.

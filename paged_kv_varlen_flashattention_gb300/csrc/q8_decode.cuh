@@ -47,7 +47,7 @@ struct Q8Params : SplitParams {
 };
 
 constexpr int kQ8MaxBoxes = 256;         // TMA boxes (32 rows or more) of one split
-constexpr int kQ8MaxSplitKeys = 8192;    // so that they suffice
+static_assert(kMaxSplitKeys <= 32 * kQ8MaxBoxes, "the boxes of the longest split");
 constexpr float kQ8Offset = 10.f;
 
 __device__ __forceinline__ bool q8_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
@@ -77,11 +77,6 @@ __device__ __forceinline__ float q8_log2_scale(float vs) {
 // no partials in memory and no second launch.  All CTAs of a cluster see the same unit, so they
 // return early together or meet at both barriers; one that gave up says so in its flag, and
 // nobody leaves before the others have read its memory.
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
-    return r;
-}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank) {
@@ -360,7 +355,6 @@ struct Q8Cfg {
     static constexpr int OFF_IDS = (OFF_FLAG + 4 + 15) & ~15;
     static constexpr int SMEM = OFF_IDS + 2 * kQ8MaxBoxes * 4 + 1024;
     static constexpr int THREADS = NW * 32 + 64;
-    static constexpr bool Q_IN_REGS = DP <= 128;
     static constexpr int MERGE = NW * (DP / 8) * 32 * 16 + NW * 32 * 16;
     static_assert(KPW % (16 * CK) == 0, "keys per warp");
     static_assert((DP / 16) % KW == 0, "columns per warp in the merge");
@@ -431,11 +425,9 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
     };
     int plain_lo = max(lo0, lo1), plain_hi = min(hi0, hi1);
     q8_plain_keys(p.alibi != nullptr, plain_lo, plain_hi);
-    uint32_t qf[C::Q_IN_REGS ? DP / 16 : 1][4];
-    if constexpr (C::Q_IN_REGS) {
+    uint32_t qf[DP / 16][4];
 #pragma unroll
-        for (int ks = 0; ks < DP / 16; ++ks) q_frag(ks, qf[ks]);
-    }
+    for (int ks = 0; ks < DP / 16; ++ks) q_frag(ks, qf[ks]);
     float o[DP / 8][4];  // [2 x unit + column parity]
 #pragma unroll
     for (int n = 0; n < DP / 8; ++n)
@@ -471,15 +463,10 @@ __device__ __forceinline__ bool decode_q8_unit(const CUtensorMap& tm_k, const CU
                     uint32_t b0, b1, b2, b3;  // (keys 0..7, k-step 2 kp), (same, 2 kp + 1), (keys 8..15, ...)
                     ldsm_x4(k_base + q8_off<DP, NT>(kk0 + rr + ((mi >> 1) << 3), 2 * kp + (mi & 1)), b0, b1, b2, b3);
                     uint32_t a0[4], a1[4];
-                    if constexpr (C::Q_IN_REGS) {
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            a0[e] = qf[2 * kp][e];
-                            a1[e] = qf[2 * kp + 1][e];
-                        }
-                    } else {
-                        q_frag(2 * kp, a0);
-                        q_frag(2 * kp + 1, a1);
+                    for (int e = 0; e < 4; ++e) {
+                        a0[e] = qf[2 * kp][e];
+                        a1[e] = qf[2 * kp + 1][e];
                     }
                     MmaOp<__half>::run(s[kc][0], a0, e4m3x2_to_half2(b0), e4m3x2_hi_to_half2(b0));
                     MmaOp<__half>::run(s[kc][1], a0, e4m3x2_to_half2(b2), e4m3x2_hi_to_half2(b2));

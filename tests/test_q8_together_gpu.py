@@ -238,3 +238,43 @@ def test_long_offsets():
     tol = (2.0 ** -9 + 2.0 ** -15) * mag + 2.0 ** -22 * vv.abs().max() * n + 2.0 ** -8 * ref.abs()
     assert ((out.cpu().double() - ref).abs() <= tol).all()
     assert ((last.cpu().double() - ref[-1:]).abs() <= tol[-1:]).all()
+
+
+@pytest.mark.parametrize("sq,D", [([1, 1], 128), ([4, 4], 128), ([1, 1], 256), ([300, 200], 256)])
+def test_bounded_waits_of_every_kernel(sq, D):
+    """Waits that run out (loads withheld): clusters of both bodies, splits of wide heads, the wide prefill.  The
+    calls end, report it, and the next call is as it should be."""
+    x = inputs(sq, [3000, 900], H=8, Hkv=2, D=D, P=64, seed=5)
+    want = call(x)
+    torch.cuda.synchronize()
+    assert binding.device_status() == 0
+    binding.set_wait_limit_ns(20_000_000)
+    binding.set_withhold_loads(True)
+    try:
+        call(x)
+        assert binding.STATUS[binding.device_status()] == "PA_ERR_DEVICE_TIMEOUT"
+    finally:
+        binding.set_withhold_loads(False)
+        binding.set_wait_limit_ns(0)
+    out, lse = call(x)
+    assert binding.device_status() == 0
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_bad_blocks_in_a_cluster():
+    """A block outside the pool in one CTA's share of a unit, and a sequence longer than promised: reported, the
+    other sequences as they should be."""
+    x = inputs([1, 1, 1], [3000, 2000, 900], H=4, Hkv=1, D=128, P=64, seed=6)
+    want = call(x)
+    torch.cuda.synchronize()
+    good = x["bt"].clone()
+    x["bt"][0, 20] = x["k"].shape[0] + 5
+    x["bt"][2, 3] = -1
+    out, _ = call(x)
+    assert binding.STATUS[binding.device_status()] == "PA_ERR_DEVICE_BOUNDS"
+    assert torch.equal(out[1], want[0][1])
+    x["bt"] = good
+    out, _ = call(x, max_sk=2000)
+    assert binding.STATUS[binding.device_status()] == "PA_ERR_DEVICE_BOUNDS"
+    out, lse = call(x)
+    assert binding.device_status() == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
