@@ -170,6 +170,14 @@ def _bind_runtime():
     return _runtime
 
 
+def _new(make, like, stream):
+    """An output of a call on ``stream`` (None: the current one), from that stream's memory."""
+    if stream is None:
+        return make(like)
+    with _runtime[0].cuda.stream(stream):
+        return make(like)
+
+
 def _call(fn, on, stream, *args) -> None:
     """fn(*args, stream) with the device of tensor ``on`` current (its current stream when
     ``stream`` is None); raises PaError on a non-zero status."""
@@ -326,7 +334,7 @@ def kv_append_rope(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_ca
     tensors = (_runtime or _bind_runtime())[3]
     P = page_block_size if page_block_size is not None else k_cache.shape[1]
     if q is not None and q_out is None:
-        q_out = tensors.empty_like(q)
+        q_out = _new(tensors.empty_like, q, stream)
     keep, *ds = tensors.pack(q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, q_out)
     _call(_lib.pa_kv_append_rope, k_new, stream, *ds[:5], 1 if interleaved else 0, *ds[5:10], int(P), ds[10])
     return q_out
@@ -348,7 +356,7 @@ def kv_append_q8(k_new, v_new, cu_seqlens_new, cu_seqlens_k, block_table, k_cach
     tensors = (_runtime or _bind_runtime())[3]
     P = page_block_size if page_block_size is not None else k_cache.shape[1]
     if q is not None and q_out is None:
-        q_out = tensors.empty_like(q)
+        q_out = _new(tensors.empty_like, q, stream)
     keep, *ds = tensors.pack(q, k_new, v_new, cos, sin, cu_seqlens_new, cu_seqlens_k, block_table, k_cache, v_cache, k_scale, v_scale,
                               q_out)
     _call(_lib.pa_kv_append_q8, k_new, stream, *ds[:5], 1 if interleaved else 0, *ds[5:12], int(P), ds[12])
@@ -376,9 +384,9 @@ def varlen_fwd_q8(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlen
     if softmax_scale is None:
         softmax_scale = shape[-1] ** -0.5
     if out is None:
-        out = tensors.empty_like(q)
+        out = _new(tensors.empty_like, q, stream)
     if softmax_lse is None:
-        softmax_lse = tensors.empty_lse(q)
+        softmax_lse = _new(tensors.empty_lse, q, stream)
     keep, *ds = tensors.pack(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cu_seqlens_k, block_table, alibi_slopes, out,
                               softmax_lse)
     _call(_lib.pa_varlen_fwd_q8, q, stream, *ds[:8], int(max_seqlen_q), int(max_seqlen_k), shape[-2], cache[-2],

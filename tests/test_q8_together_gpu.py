@@ -278,3 +278,17 @@ def test_bad_blocks_in_a_cluster():
     assert binding.STATUS[binding.device_status()] == "PA_ERR_DEVICE_BOUNDS"
     out, lse = call(x)
     assert binding.device_status() == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_outputs_of_a_call_on_a_given_stream():
+    """Outputs that a call allocates come from the memory of the stream it is given, and hold its results."""
+    s = Server(2, 4, seed=9)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    r = s.step([100, 1], stream=side)
+    side.synchronize()
+    s.check(r)
+    segments = torch.cuda.memory_snapshot()
+    for t in r[:3]:
+        own = [g for g in segments if g["address"] <= t.data_ptr() < g["address"] + g["total_size"]]
+        assert len(own) == 1 and own[0]["stream"] == side.cuda_stream
